@@ -78,6 +78,9 @@ typedef struct CUstream_st* rz_stream_t;  /* == cudaStream_t */
 #define RZ_DEVERR_CU_SEQLENS   2  /* cu_seqlens not 0 = cu[0] <= ... <= cu[B] = T */
 #define RZ_DEVERR_TIMEOUT      4  /* a pipeline wait gave up (kernel returned early) */
 #define RZ_DEVERR_RANGE        8  /* a reference log-sum-exp too far from the row's (rz_loss_fwd_bwd_ref) */
+#define RZ_DEVERR_PAGES       16  /* a page id, a length or a slot outside its table, pool or buffer */
+#define RZ_DEVERR_LOGITS      32  /* a row without a finite logit, or with a NaN or +inf (rz_filter_sample) */
+#define RZ_DEVERR_PARAM       64  /* a row's temperature, top-p, min-p or uniform out of its range */
 
 /* Operation ids for rz_workspace_size(). */
 #define RZ_OP_TOKEN_LOGPROB   0
@@ -87,6 +90,12 @@ typedef struct CUstream_st* rz_stream_t;  /* == cudaStream_t */
 #define RZ_OP_SAMPLE          4
 #define RZ_OP_SC_LOSS_FWD_BWD 5
 #define RZ_OP_LOSS_FWD_BWD_REF 6  /* rz_loss_fwd_bwd_ref, and rz_loss_fwd_bwd_shard with ref_lse */
+#define RZ_OP_GROUP_DECODE_ATTN 7 /* T = requests, d = head size, V = query heads, B = prompts */
+
+/* Element types of the operators that take more than one. */
+#define RZ_DTYPE_F32  0
+#define RZ_DTYPE_BF16 1
+#define RZ_DTYPE_F16  2
 
 /*
  * Bytes of scratch the operation needs for these sizes (0 if none).  Pure
@@ -372,6 +381,159 @@ RZ_API int rz_logits_loss_fwd_bwd(rz_bf16* logits_inout, const int32_t* tokens,
                            float* loss_out, float* d3_out, float* logprob_out,
                            void* ws, size_t ws_bytes, int32_t* err_flag,
                            rz_stream_t stream);
+
+/*
+ * ------------------------------------------------------------------------
+ * Rollouts of response groups: the paged cache's tables, attention over a
+ * prompt shared by its group, filtered sampling and the logprob under what
+ * the filter kept.  The pages have no counterpart for these four: they are
+ * what a rollout of groups (G responses to one prompt [vLLM-zh s.4 item 3])
+ * with sampling filters needs around the logprob path, on both of its sides.
+ * ------------------------------------------------------------------------
+ */
+
+/*
+ * Block tables and the slot map of the tokens a step adds, from the
+ * requests' lengths alone (no host round trip; capturable).
+ *   lens [B] int32        tokens of request i already in the cache; the pages
+ *                         of those, ceil(lens_i / page_size), stand in its row
+ *   new_lens [B] int32    tokens it adds now
+ *   free_pages [n_free] int32   page ids to hand out
+ *   table [B, width] int32 in place: entries ceil(lens_i/p) ..
+ *                         ceil((lens_i + new_i)/p) - 1 of row i become the
+ *                         next free pages, requests in order; every other
+ *                         entry is left as it is
+ *   slots_out [n_slots] int64   for the packed new tokens t = cu_i .. cu_i+1-1,
+ *                         position pos = lens_i + t - cu_i:
+ *                         table[i, pos / p] * p + pos % p; -1 past cu_B
+ *                         (a buffer larger than the step, for a CUDA graph)
+ *   cu_out [B+1] int64    exclusive sums of new_lens
+ *   used_out [1] int32    free pages the step needs (the caller moves on by
+ *                         it; more than n_free when they ran out)
+ * The call is idempotent: the same lengths and free list give the same rows.
+ * A negative length counts as 0; a position past the row's width, a page
+ * past the free list, a negative page id in a row and a token past n_slots
+ * get slot (and table entry) -1 or are dropped, and set RZ_DEVERR_PAGES.
+ * B, n_free, n_slots >= 0; page_size, width >= 1; B * width < 2^31.
+ * One launch while one block can do it all (B <= 1024 and n_slots <= 16384),
+ * else two.  No workspace.  slots_out may be null if n_slots = 0.
+ */
+RZ_API int rz_page_tables(const int32_t* lens, const int32_t* new_lens, int32_t B,
+                          const int32_t* free_pages, int64_t n_free, int32_t page_size,
+                          int32_t* table, int32_t width, int64_t* slots_out, int64_t n_slots,
+                          int64_t* cu_out, int32_t* used_out, int32_t* err_flag,
+                          rz_stream_t stream);
+
+/*
+ * Decode attention of response groups: one query token per request, over its
+ * prompt's shared cache pages and its own pages.
+ *   q [B, Hq, D]      dtype RZ_DTYPE_BF16 or RZ_DTYPE_F16; strides in elements
+ *                     q_stride = {request, head}, D contiguous
+ *   k_cache, v_cache  [n_pages, page_size, Hkv, D], the same dtype; strides
+ *                     kv_stride = {K page, K token, K head, V page, V token,
+ *                     V head} in elements, D contiguous; offsets in 64 bits
+ *   prefix_table [P, prefix_width] int32, prefix_lens [P] int32: each
+ *                     prompt's pages and tokens
+ *   cu_group [P+1] int32: requests cu_group[g] .. cu_group[g+1]-1 answer
+ *                     prompt g (a group may be empty; a request in no group
+ *                     has no prefix).  P = 0: all three may be null.
+ *   table [B, width] int32, lens [B] int32: each request's own pages and
+ *                     tokens (the new token's K and V already in them)
+ *   out [B, Hq, D] contiguous, same dtype;  lse_out [B, Hq] fp32 (nullable)
+ *     s_j = scale q . k_j,  lse = log sum_j e^(s_j),  out = sum_j e^(s_j - lse) v_j
+ *   over the prefix tokens and the own tokens; query head h reads KV head
+ *   h / (Hq / Hkv).  No token at all: out = 0, lse = -inf.
+ * A prefix's K and V are read once for its whole group (once per 128 query
+ * rows of a KV head).  Products of the 16-bit inputs on the tensor cores,
+ * scores, softmax statistics and the output's sums in fp32, the softmax terms
+ * rounded to the inputs' type as the second product's operand.
+ * Requires: Hq % Hkv == 0, Hq / Hkv <= 128, D % 8 == 0, 8 <= D <= 128, and
+ * 16-byte alignment of q, k_cache, v_cache, out and all strides
+ * (RZ_ERR_UNSUPPORTED otherwise); B, P >= 0.
+ * Lengths past a row's width or negative are cut, page ids outside
+ * [0, n_pages) are skipped, a cu_group that is not 0 <= cu[0] <= ... <= B is
+ * cut to it: RZ_DEVERR_PAGES / RZ_DEVERR_CU_SEQLENS, no access leaves the
+ * arrays.  Results do not change from run to run.  Workspace:
+ * rz_workspace_size(RZ_OP_GROUP_DECODE_ATTN, B, D, Hq, P).
+ */
+RZ_API int rz_group_decode_attn(const void* q, const int64_t* q_stride, const void* k_cache,
+                                const void* v_cache, const int64_t* kv_stride, int32_t n_pages,
+                                int32_t page_size, const int32_t* prefix_table,
+                                int32_t prefix_width, const int32_t* prefix_lens,
+                                const int32_t* cu_group, int32_t P, const int32_t* table,
+                                int32_t width, const int32_t* lens, int32_t B, int32_t Hq,
+                                int32_t Hkv, int32_t D, int32_t dtype, float scale, void* out,
+                                float* lse_out, void* ws, size_t ws_bytes, int32_t* err_flag,
+                                rz_stream_t stream);
+
+/*
+ * Rollout side with sampling filters: draws a_t from softmax(z_t / tau_t) cut
+ * to what top-k, top-p and min-p keep, from a given uniform per row, and
+ * records log mu(a_t) under the kept tokens.
+ *   logits [T, V]     dtype RZ_DTYPE_*, row stride ld >= V elements
+ *   temperature [T]   fp32 (nullable: 1): 0 (greedy: the likeliest token) or
+ *                     2^-20 .. 2^20
+ *   top_k [T] int32   (nullable) k <= 0 or >= V keeps all
+ *   top_p [T] fp32    (nullable) p >= 1 keeps all, p <= 0 the first token
+ *   min_p [T] fp32    (nullable) <= 0 keeps all; at most 1
+ *   uniform [T] fp32  in [0, 1)
+ * The order of a row: logits descending, ties by the lowest index.  Kept are
+ * the first k of it; of these the shortest head whose probability is at
+ * least p times theirs; of these every token with a probability of at least
+ * min_p times the likeliest's.  -inf logits are never kept.  The token is
+ * the first v, in the order of the vocabulary, at which the kept
+ * probabilities' running sum passes u times their total.
+ *   tokens_out [T] int32, logprob_out [T] fp32 (log mu), kept_out [T] int32
+ *   (nullable: how many were kept), keep_out [T, ceil(V/32)] uint32
+ *   (nullable: bit v % 32 of word v / 32 says that v was kept)
+ * The sums behind every decision are 64-bit integers: weights
+ * e^((z - max z)/tau) rounded to 2^-44 (V <= 2^18) with a relative error of
+ * about 2^-35, added exactly.  So a row's result does not depend on its batch,
+ * and equals that of exact arithmetic but for borders that close.
+ * logprob_out is bitwise what rz_keep_logprob gives for the same logits,
+ * token, temperature and keep_out.
+ * A row with a NaN, a +inf or no finite logit (RZ_DEVERR_LOGITS), or a
+ * parameter out of its range (RZ_DEVERR_PARAM): token -1, log mu NaN, none kept.
+ * T >= 0, 1 <= V <= 2^24.  No workspace.
+ */
+RZ_API int rz_filter_sample(const void* logits, int64_t ld, int32_t dtype, int64_t T, int32_t V,
+                            const float* temperature, const int32_t* top_k, const float* top_p,
+                            const float* min_p, const float* uniform, int32_t* tokens_out,
+                            float* logprob_out, int32_t* kept_out, uint32_t* keep_out,
+                            int32_t* err_flag, rz_stream_t stream);
+
+/*
+ * Learner side of a filtered rollout: the log-probability of given tokens
+ * under softmax(z_t / tau_t) cut to a given kept set (keep_out of the rollout,
+ * so that learner and rollout compare distributions over the same tokens).
+ *   logits, ld, dtype, temperature (0 counts as 1) as above
+ *   tokens [T] int32
+ *   keep [T, ceil(V/32)] uint32 (nullable: all of the vocabulary); logits of
+ *                     tokens not kept are not looked at (they may hold NaN)
+ *   lse_out [T] fp32 (nullable)  log sum_{v kept} e^(z_v / tau)
+ *   logprob_out [T] fp32         z_a / tau - lse; -inf for a token not kept
+ * Nothing kept, or only -inf: lse = logprob = -inf.  A token outside [0, V)
+ * gives NaN and RZ_DEVERR_TOKEN_RANGE, a temperature out of range NaN and
+ * RZ_DEVERR_PARAM.  A row's result does not depend on its batch.  No workspace.
+ */
+RZ_API int rz_keep_logprob(const void* logits, int64_t ld, int32_t dtype, int64_t T, int32_t V,
+                           const uint32_t* keep, const float* temperature, const int32_t* tokens,
+                           float* logprob_out, float* lse_out, int32_t* err_flag,
+                           rz_stream_t stream);
+
+/*
+ * Its gradient with respect to the logits, for dlogprob [T] fp32 (for the
+ * importance-sampled loss: minus rz_is_loss's coef_out):
+ *   dlogits_tv = (g_t / tau_t) ([v = a_t] - [v kept] e^(z_tv / tau_t - lse_t))
+ * lse [T] is rz_keep_logprob's.  dlogits [T, V] has the logits' dtype, row
+ * stride ldd, and may be the logits themselves (ldd = ld).  Every entry of
+ * [T, V] is written.  A row whose token is not kept (or outside [0, V)), whose
+ * lse is not finite or whose g is 0 gets zeros.  No workspace.
+ */
+RZ_API int rz_keep_logprob_bwd(const void* logits, int64_t ld, int32_t dtype, int64_t T,
+                               int32_t V, const uint32_t* keep, const float* temperature,
+                               const int32_t* tokens, const float* lse, const float* dlogprob,
+                               void* dlogits, int64_t ldd, int32_t* err_flag, rz_stream_t stream);
 
 /*
  * LM-head logits z = H W^T as fp32 [T, V] (row-major), from the same

@@ -31,6 +31,13 @@ RZ_DEVERR_TOKEN_RANGE = 1
 RZ_DEVERR_CU_SEQLENS = 2
 RZ_DEVERR_TIMEOUT = 4
 RZ_DEVERR_RANGE = 8
+RZ_DEVERR_PAGES = 16
+RZ_DEVERR_LOGITS = 32
+RZ_DEVERR_PARAM = 64
+
+RZ_DTYPE_F32 = 0
+RZ_DTYPE_BF16 = 1
+RZ_DTYPE_F16 = 2
 
 RZ_PROF_NAMES = ("logprob_gemm", "keep_gemm", "merge", "dz", "dH_gemm", "dW_gemm",
                  "logits_rows", "small")  # index = RZ_PROF_* class
@@ -42,6 +49,7 @@ RZ_OP_IS_LOSS = 3
 RZ_OP_SAMPLE = 4
 RZ_OP_SC_LOSS_FWD_BWD = 5
 RZ_OP_LOSS_FWD_BWD_REF = 6
+RZ_OP_GROUP_DECODE_ATTN = 7
 
 _lib = None
 
@@ -79,6 +87,16 @@ _SIGNATURES = {
     "rz_profile_begin": (ctypes.c_int, []),
     "rz_debug_check_failures": (ctypes.c_int, [_P, _P]),
     "rz_profile_end": (ctypes.c_int, [_P, _P, _I32]),
+    "rz_page_tables": (ctypes.c_int, [_P, _P, _I32, _P, _I64, _I32, _P, _I32, _P, _I64, _P, _P,
+                                      _P, _P]),
+    "rz_group_decode_attn": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _I32, _P, _I32, _P, _P,
+                                            _I32, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32,
+                                            ctypes.c_float, _P, _P, _P, _SZ, _P, _P]),
+    "rz_filter_sample": (ctypes.c_int, [_P, _I64, _I32, _I64, _I32, _P, _P, _P, _P, _P, _P, _P,
+                                        _P, _P, _P, _P]),
+    "rz_keep_logprob": (ctypes.c_int, [_P, _I64, _I32, _I64, _I32, _P, _P, _P, _P, _P, _P, _P]),
+    "rz_keep_logprob_bwd": (ctypes.c_int, [_P, _I64, _I32, _I64, _I32, _P, _P, _P, _P, _P, _P,
+                                           _I64, _P, _P]),
 }
 
 
@@ -625,6 +643,270 @@ def rz_sample_logprob(H, W, seed, row_ids=None, tokens_out=None, logprob_out=Non
                                _ws_bytes(ws), _ptr(err_flag), _stream(stream))
     _check("rz_sample_logprob", st)
     return tokens_out, logprob_out
+
+
+# ------------------------------------------------------- rollouts of response groups
+def _dtype_id(t, name, allowed):
+    torch = _torch()
+    ids = {torch.float32: RZ_DTYPE_F32, torch.bfloat16: RZ_DTYPE_BF16, torch.float16: RZ_DTYPE_F16}
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or ids.get(t.dtype) not in allowed:
+        names = {v: str(k) for k, v in ids.items()}
+        raise TypeError("%s must be a CUDA tensor of %s"
+                        % (name, " or ".join(names[i] for i in allowed)))
+    return ids[t.dtype]
+
+
+def _new(shape, dtype, device, stream):
+    """An output or workspace for work on `stream`: allocated there, so that
+    its memory is neither still in use by nor handed on to another stream."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(t, name):
+    """[T, V] with contiguous rows; returns (dtype id, T, V, row stride)."""
+    dt = _dtype_id(t, name, (RZ_DTYPE_F32, RZ_DTYPE_BF16, RZ_DTYPE_F16))
+    if t.dim() != 2 or t.shape[1] < 1:
+        raise ValueError("%s must have shape [T, V] with V >= 1, got %s" % (name, tuple(t.shape)))
+    T, V = t.shape
+    ld = t.stride(0) if T > 1 else V
+    if (t.stride(1) != 1 and V > 1) or ld < V:
+        raise ValueError("%s must have contiguous rows that do not overlap, got strides %s"
+                         % (name, t.stride()))
+    return dt, T, V, ld
+
+
+def _row_params(T, **tensors):
+    """Optional per-row parameters: contiguous CUDA tensors [T] of a dtype."""
+    for name, (t, dtype) in tensors.items():
+        if t is not None:
+            _need(t, dtype, name)
+            _shape(t, (T,), name)
+
+
+def rz_page_tables(lens, new_lens, free_pages, page_size, table, n_slots, slots_out=None,
+                   cu_out=None, used_out=None, err_flag=None, stream=None):
+    """Extend the block tables (in place) by the pages that new_lens tokens
+    need and map those tokens to cache slots (see include/rz.h).  n_slots is
+    the slot buffer's size: the tokens added, or more (the rest gets -1).
+    Returns (slots [n_slots] int64, cu [B+1] int64, used [1] int32)."""
+    torch = _torch()
+    lib = load()
+    _need(lens, torch.int32, "lens")
+    _need(new_lens, torch.int32, "new_lens")
+    _need(free_pages, torch.int32, "free_pages")
+    _need(table, torch.int32, "table")
+    if table.dim() != 2:
+        raise ValueError("table must have shape [B, width], got %s" % (tuple(table.shape),))
+    B, width = table.shape
+    n_slots = int(n_slots)
+    _shape(lens, (B,), "lens")
+    _shape(new_lens, (B,), "new_lens")
+    _out(slots_out, torch.int64, "slots_out", (n_slots,))
+    _out(cu_out, torch.int64, "cu_out", (B + 1,))
+    _out(used_out, torch.int32, "used_out")
+    _out(err_flag, torch.int32, "err_flag")
+    _same_device(lens, new_lens, free_pages, table, slots_out, cu_out, used_out, err_flag)
+    strm = _stream(stream)
+    if n_slots < 0:
+        raise ValueError("n_slots must not be negative")
+    dev = table.device
+    if slots_out is None:
+        slots_out = _new(n_slots, torch.int64, dev, stream)
+    if cu_out is None:
+        cu_out = _new(B + 1, torch.int64, dev, stream)
+    if used_out is None:
+        used_out = _new(1, torch.int32, dev, stream)
+    st = lib.rz_page_tables(_ptr(lens), _ptr(new_lens), B, _ptr(free_pages), free_pages.numel(),
+                            int(page_size), _ptr(table), width, _ptr(slots_out), n_slots,
+                            _ptr(cu_out), _ptr(used_out), _ptr(err_flag), strm)
+    _check("rz_page_tables", st)
+    return slots_out, cu_out, used_out
+
+
+def rz_group_decode_attn(q, k_cache, v_cache, table, lens, prefix_table=None, prefix_lens=None,
+                         cu_group=None, scale=None, out=None, lse_out=None, ws=None,
+                         err_flag=None, stream=None):
+    """Decode attention of response groups over their prompt's shared pages
+    and their own (see include/rz.h).  q [B, Hq, D] and k_cache, v_cache
+    [n_pages, page, Hkv, D] may be strided (the head size contiguous); scale
+    defaults to D ** -0.5.  Returns (out [B, Hq, D], lse [B, Hq] fp32)."""
+    torch = _torch()
+    lib = load()
+    dt = _dtype_id(q, "q", (RZ_DTYPE_BF16, RZ_DTYPE_F16))
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _dtype_id(t, name, (dt,))
+        if t.dim() != 4 or t.shape[1] < 1:
+            raise ValueError("%s must have shape [n_pages, page, Hkv, D], got %s"
+                             % (name, tuple(t.shape)))
+    if q.dim() != 3:
+        raise ValueError("q must have shape [B, Hq, D], got %s" % (tuple(q.shape),))
+    B, Hq, D = q.shape
+    n_pages, page, Hkv, _ = k_cache.shape
+    _shape(k_cache, (n_pages, page, Hkv, D), "k_cache")
+    _shape(v_cache, (n_pages, page, Hkv, D), "v_cache")
+    for t, name in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.stride(-1) != 1 and D > 1:
+            raise ValueError("%s must be contiguous along the head size, got strides %s"
+                             % (name, t.stride()))
+        if any(x < 0 for x in t.stride()):
+            raise ValueError("%s has a negative stride" % name)
+    _need(table, torch.int32, "table")
+    _need(lens, torch.int32, "lens")
+    if table.dim() != 2:
+        raise ValueError("table must have shape [B, width], got %s" % (tuple(table.shape),))
+    _shape(table, (B, table.shape[1]), "table")
+    _shape(lens, (B,), "lens")
+    group = (prefix_table, prefix_lens, cu_group)
+    if any(t is None for t in group) != all(t is None for t in group):
+        raise TypeError("prefix_table, prefix_lens and cu_group come together")
+    P, prefix_width = 0, 0
+    if prefix_table is not None:
+        _need(prefix_table, torch.int32, "prefix_table")
+        _need(prefix_lens, torch.int32, "prefix_lens")
+        _need(cu_group, torch.int32, "cu_group")
+        if prefix_table.dim() != 2:
+            raise ValueError("prefix_table must have shape [P, width], got %s"
+                             % (tuple(prefix_table.shape),))
+        P, prefix_width = prefix_table.shape
+        _shape(prefix_lens, (P,), "prefix_lens")
+        _shape(cu_group, (P + 1,), "cu_group")
+    _out(out, q.dtype, "out", (B, Hq, D))
+    _out(lse_out, torch.float32, "lse_out", (B, Hq))
+    _out(err_flag, torch.int32, "err_flag")
+    _same_device(q, k_cache, v_cache, table, lens, prefix_table, prefix_lens, cu_group, out,
+                 lse_out, ws, err_flag)
+    strm = _stream(stream)
+    if ws is None:
+        n = workspace_size(RZ_OP_GROUP_DECODE_ATTN, B, D, Hq, P)
+        ws = _new(max(n, 256), torch.uint8, q.device, stream)
+    ws_bytes = _ws_bytes(ws)
+    if out is None:
+        out = _new((B, Hq, D), q.dtype, q.device, stream)
+    if lse_out is None:
+        lse_out = _new((B, Hq), torch.float32, q.device, stream)
+    # strides of axes that hold one element mean nothing: give them as 0
+    step = lambda t, i: t.stride(i) if t.shape[i] > 1 else 0  # noqa: E731
+    qs = (ctypes.c_int64 * 2)(step(q, 0), step(q, 1))
+    kvs = (ctypes.c_int64 * 6)(*[step(t, i) for t in (k_cache, v_cache) for i in range(3)])
+    st = lib.rz_group_decode_attn(_ptr(q), qs, _ptr(k_cache), _ptr(v_cache), kvs, n_pages, page,
+                                  _ptr(prefix_table), prefix_width, _ptr(prefix_lens),
+                                  _ptr(cu_group), P, _ptr(table), table.shape[1], _ptr(lens), B,
+                                  Hq, Hkv, D, dt, float(D ** -0.5 if scale is None else scale),
+                                  _ptr(out), _ptr(lse_out), _ptr(ws), ws_bytes, _ptr(err_flag),
+                                  strm)
+    _check("rz_group_decode_attn", st)
+    return out, lse_out
+
+
+def rz_filter_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None,
+                     tokens_out=None, logprob_out=None, kept_out=None, keep_out=None,
+                     want_keep=False, err_flag=None, stream=None):
+    """Sample a token a row under temperature, top-k, top-p and min-p from a
+    given uniform (see include/rz.h).  logits [T, V] fp32, bf16 or fp16 with
+    contiguous rows.  Returns (tokens [T] int32, log mu [T] fp32, kept [T]
+    int32, keep): keep is the kept set as [T, ceil(V/32)] int32 words (bit v %
+    32 of word v // 32) if keep_out or want_keep asks for it, else None."""
+    torch = _torch()
+    lib = load()
+    dt, T, V, ld = _rows(logits, "logits")
+    if uniform is None:
+        raise TypeError("uniform must be a contiguous CUDA tensor of torch.float32")
+    _row_params(T, uniform=(uniform, torch.float32), temperature=(temperature, torch.float32),
+                top_k=(top_k, torch.int32), top_p=(top_p, torch.float32),
+                min_p=(min_p, torch.float32))
+    words = (V + 31) // 32
+    _out(tokens_out, torch.int32, "tokens_out", (T,))
+    _out(logprob_out, torch.float32, "logprob_out", (T,))
+    _out(kept_out, torch.int32, "kept_out", (T,))
+    _out(keep_out, torch.int32, "keep_out", (T, words))
+    _out(err_flag, torch.int32, "err_flag")
+    _same_device(logits, uniform, temperature, top_k, top_p, min_p, tokens_out, logprob_out,
+                 kept_out, keep_out, err_flag)
+    strm = _stream(stream)
+    dev = logits.device
+    if tokens_out is None:
+        tokens_out = _new(T, torch.int32, dev, stream)
+    if logprob_out is None:
+        logprob_out = _new(T, torch.float32, dev, stream)
+    if kept_out is None:
+        kept_out = _new(T, torch.int32, dev, stream)
+    if keep_out is None and want_keep:
+        keep_out = _new((T, words), torch.int32, dev, stream)
+    st = lib.rz_filter_sample(_ptr(logits), ld, dt, T, V, _ptr(temperature), _ptr(top_k),
+                              _ptr(top_p), _ptr(min_p), _ptr(uniform), _ptr(tokens_out),
+                              _ptr(logprob_out), _ptr(kept_out), _ptr(keep_out), _ptr(err_flag),
+                              strm)
+    _check("rz_filter_sample", st)
+    return tokens_out, logprob_out, kept_out, keep_out
+
+
+def _keep_rows(logits, tokens, keep, temperature):
+    torch = _torch()
+    dt, T, V, ld = _rows(logits, "logits")
+    _need(tokens, torch.int32, "tokens")
+    _shape(tokens, (T,), "tokens")
+    _row_params(T, temperature=(temperature, torch.float32))
+    if keep is not None:
+        _need(keep, torch.int32, "keep")
+        _shape(keep, (T, (V + 31) // 32), "keep")
+    return dt, T, V, ld
+
+
+def rz_keep_logprob(logits, tokens, keep=None, temperature=None, logprob_out=None, lse_out=None,
+                    err_flag=None, stream=None):
+    """Log-probability of given tokens under softmax(logits / temperature) cut
+    to a kept set, as rz_filter_sample returns it (see include/rz.h).
+    Returns (logprob [T] fp32, lse [T] fp32)."""
+    torch = _torch()
+    lib = load()
+    dt, T, V, ld = _keep_rows(logits, tokens, keep, temperature)
+    _out(logprob_out, torch.float32, "logprob_out", (T,))
+    _out(lse_out, torch.float32, "lse_out", (T,))
+    _out(err_flag, torch.int32, "err_flag")
+    _same_device(logits, tokens, keep, temperature, logprob_out, lse_out, err_flag)
+    strm = _stream(stream)
+    if logprob_out is None:
+        logprob_out = _new(T, torch.float32, logits.device, stream)
+    if lse_out is None:
+        lse_out = _new(T, torch.float32, logits.device, stream)
+    st = lib.rz_keep_logprob(_ptr(logits), ld, dt, T, V, _ptr(keep), _ptr(temperature),
+                             _ptr(tokens), _ptr(logprob_out), _ptr(lse_out), _ptr(err_flag), strm)
+    _check("rz_keep_logprob", st)
+    return logprob_out, lse_out
+
+
+def rz_keep_logprob_bwd(logits, tokens, lse, dlogprob, keep=None, temperature=None,
+                        dlogits_out=None, err_flag=None, stream=None):
+    """Gradient of rz_keep_logprob with respect to the logits, for dlogprob
+    [T] fp32 (see include/rz.h).  dlogits_out may be the logits themselves.
+    Returns dlogits [T, V] in the logits' dtype."""
+    torch = _torch()
+    lib = load()
+    dt, T, V, ld = _keep_rows(logits, tokens, keep, temperature)
+    _need(lse, torch.float32, "lse")
+    _shape(lse, (T,), "lse")
+    _need(dlogprob, torch.float32, "dlogprob")
+    _shape(dlogprob, (T,), "dlogprob")
+    ldd = V
+    if dlogits_out is not None:
+        got, _, _, ldd = _rows(dlogits_out, "dlogits_out")
+        _shape(dlogits_out, (T, V), "dlogits_out")
+        if got != dt:
+            raise TypeError("dlogits_out must have the dtype of logits, %s" % logits.dtype)
+    _out(err_flag, torch.int32, "err_flag")
+    _same_device(logits, tokens, lse, dlogprob, keep, temperature, dlogits_out, err_flag)
+    strm = _stream(stream)
+    if dlogits_out is None:
+        dlogits_out = _new((T, V), logits.dtype, logits.device, stream)
+    st = lib.rz_keep_logprob_bwd(_ptr(logits), ld, dt, T, V, _ptr(keep), _ptr(temperature),
+                                 _ptr(tokens), _ptr(lse), _ptr(dlogprob), _ptr(dlogits_out), ldd,
+                                 _ptr(err_flag), strm)
+    _check("rz_keep_logprob_bwd", st)
+    return dlogits_out
 
 
 def rz_selftest_wait_timeout(err_flag, done_out=None, limit_us=50000, stream=None):

@@ -1,0 +1,313 @@
+// rz_keep.cu -- the log-probability of given tokens under a kept set of each
+// row's vocabulary, and its gradient with respect to the logits.
+//
+//   lse = log sum_{v kept} e^(z_v / tau),   log p = z_a / tau - lse,
+//   dz_v = (g / tau) ([v = a] - [v kept] e^(z_v / tau - lse)).
+//
+// Both are bandwidth-bound: forward reads the mask and the kept logits,
+// backward the same again and writes a dense row.  A lane looks at the mask
+// byte of its eight columns first and loads logits only where a bit is set: at
+// some tens of kept tokens in 151,936 nearly all of the logits stay unread.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "rz.h"
+#include "rz_internal.h"
+#include "rz_keep.cuh"
+
+namespace rz {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kKeepThreads = 256;
+constexpr int kKeepWarps = kKeepThreads / 32;
+constexpr int kMaxCluster = 8;
+
+struct KeepArgs {
+  const void* logits;
+  long long ld;
+  const uint32_t* keep;  // nullable
+  const float* temperature;
+  const int32_t* tokens;
+  float *logprob, *lse;             // forward
+  const float *lse_in, *dlogprob;   // backward
+  void* dlogits;
+  long long ldd;
+  int* err;
+  long long T;
+  int V, words, chunks;
+};
+
+struct MaskKept {
+  const uint32_t* words;  // of the row; null: all
+  int V;
+  __device__ __forceinline__ uint32_t before(int col) const {
+    const uint32_t in = V - col >= 8 ? 0xffu : (1u << (V - col)) - 1u;
+    return words ? reinterpret_cast<const uint8_t*>(words)[col >> 3] & in : in;
+  }
+  template <class A>
+  __device__ __forceinline__ uint32_t after(int, const A&, uint32_t bits) const {
+    return bits;
+  }
+  __device__ __forceinline__ bool has(int v) const {
+    return !words || ((words[v >> 5] >> (v & 31)) & 1u);
+  }
+};
+
+// Whether a chunk has any kept column (warp-uniform): its 64 words at once.
+__device__ __forceinline__ bool chunk_any(const uint32_t* words, int n_words, int chunk) {
+  if (!words) return true;
+  const int w = chunk * (kKeepChunk / 32) + (threadIdx.x & 31);
+  uint32_t x = w < n_words ? words[w] : 0u;
+  if (w + 32 < n_words) x |= words[w + 32];
+  return __any_sync(0xffffffffu, x != 0);
+}
+
+template <class E>
+__global__ void __launch_bounds__(kKeepThreads, 2) keep_logprob_kernel(const KeepArgs a) {
+  extern __shared__ float2 states[];  // of the whole row, in the first CTA of the cluster
+  cg::cluster_group cluster = cg::this_cluster();
+  const int parts = static_cast<int>(cluster.num_blocks());
+  const int part = static_cast<int>(cluster.block_rank());
+  const long long row = blockIdx.x / parts;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const E* z = static_cast<const E*>(a.logits) + row * a.ld;
+  const bool vec = row_aligned(z);
+  const MaskKept kept{a.keep ? a.keep + row * a.words : nullptr, a.V};
+  const float tau = row_tau(a.temperature, row);
+  const float c = keep_scale(tau);
+  float2* dst = cluster.map_shared_rank(states, 0);
+  if (parts > 1) cluster.sync();  // every CTA of the cluster runs before its memory is written
+  for (int ch = part * kKeepWarps + warp; ch < a.chunks; ch += parts * kKeepWarps) {
+    float2 st = make_float2(-INFINITY, 0.f);
+    if (chunk_any(kept.words, a.words, ch)) st = keep_fold(z, vec, a.V, ch, c, kept);
+    if (lane == 0) dst[ch] = st;
+  }
+  if (parts > 1) cluster.sync();
+  else __syncthreads();
+  if (part != 0 || warp != 0) return;
+  const float2 st = keep_merge(states, a.chunks, c);
+  if (lane == 0) {
+    const int t = a.tokens[row];
+    float lp, lse = keep_lse_of(st, tau);
+    if (t < 0 || t >= a.V) {
+      lp = __int_as_float(0x7fc00000);
+      if (a.err) atomicOr(a.err, RZ_DEVERR_TOKEN_RANGE);
+    } else if (!kept.has(t)) {
+      lp = -INFINITY;
+    } else {
+      const float za = to_f32(z[t]);
+      lp = za == -INFINITY ? -INFINITY : keep_logprob_of(za, st, tau);
+    }
+    if (st.x == -INFINITY && st.y == 0.f) {
+      lse = -INFINITY;  // nothing kept, or only -inf
+      if (lp == lp) lp = -INFINITY;
+    }
+    if (!(tau == tau)) {
+      lp = lse = tau;
+      if (a.err) atomicOr(a.err, RZ_DEVERR_PARAM);
+    }
+    a.logprob[row] = lp;
+    if (a.lse) a.lse[row] = lse;
+  }
+}
+
+__device__ __forceinline__ void pack8(const float (&g)[8], uint4* q, float) {
+  q[0] = make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]),
+                    __float_as_uint(g[3]));
+  q[1] = make_uint4(__float_as_uint(g[4]), __float_as_uint(g[5]), __float_as_uint(g[6]),
+                    __float_as_uint(g[7]));
+}
+__device__ __forceinline__ void pack8(const float (&g)[8], uint4* q, __nv_bfloat16) {
+  *q = make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]),
+                  pack_bf16x2(g[6], g[7]));
+}
+__device__ __forceinline__ void pack8(const float (&g)[8], uint4* q, __half) {
+  *q = make_uint4(pack_f16x2(g[0], g[1]), pack_f16x2(g[2], g[3]), pack_f16x2(g[4], g[5]),
+                  pack_f16x2(g[6], g[7]));
+}
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void put(__half* p, float x) { *p = __float2half_rn(x); }
+
+template <class E>
+__device__ __forceinline__ void store8(E* row, bool vec, int V, int col, const float (&g)[8]) {
+  if (vec && col + 8 <= V) {
+    uint4 q[sizeof(E) / 2];
+    pack8(g, q, E());
+    uint4* p = reinterpret_cast<uint4*>(row + col);
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(E) / 2); ++i) p[i] = q[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i < V) put(row + col + i, g[i]);
+  }
+}
+
+template <class E>
+__global__ void __launch_bounds__(kKeepThreads) keep_logprob_bwd_kernel(const KeepArgs a) {
+  const long long row = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // not restrict: dlogits may be the logits; every lane loads its columns
+  // before it stores them, and no other lane reads them
+  const E* z = static_cast<const E*>(a.logits) + row * a.ld;
+  E* out = static_cast<E*>(a.dlogits) + row * a.ldd;
+  const bool vec = row_aligned(z), vec_out = row_aligned(out);
+  const MaskKept kept{a.keep ? a.keep + row * a.words : nullptr, a.V};
+  const float tau = row_tau(a.temperature, row);
+  const float lse = a.lse_in[row];
+  const int t = a.tokens[row];
+  const bool in = t >= 0 && t < a.V;
+  float g = a.dlogprob[row];
+  if (!in || !kept.has(t) || !isfinite(lse) || !(tau == tau)) g = 0.f;
+  if (a.err && blockIdx.y == 0 && threadIdx.x == 0) {
+    if (!in) atomicOr(a.err, RZ_DEVERR_TOKEN_RANGE);
+    if (!(tau == tau)) atomicOr(a.err, RZ_DEVERR_PARAM);
+  }
+  const float c = keep_scale(tau);
+  const float lse2 = __fmul_rn(lse, kLog2e);
+  const float gt = g / tau;
+  const int step = kKeepWarps * gridDim.y;
+  for (int ch = blockIdx.y * kKeepWarps + warp; ch < a.chunks; ch += step) {
+    const bool any = g != 0.f && chunk_any(kept.words, a.words, ch);
+#pragma unroll 2
+    for (int j = 0; j < 8; ++j) {
+      const int col = ch * kKeepChunk + 256 * j + 8 * lane;
+      if (col >= a.V) break;
+      float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      const uint32_t bits = any ? kept.before(col) : 0u;
+      if (bits) {
+        float v[8];
+        load8(z, vec, a.V, col, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (!((bits >> i) & 1u)) continue;
+          const float p = ex2_approx(fmaf(v[i], c, -lse2));
+          // at the token -(p - 1), without the cancellation as p -> 1
+          d[i] = col + i == t ? -gt * expm1f(__fsub_rn(__fdiv_rn(v[i], tau), lse)) : -gt * p;
+        }
+      }
+      store8(out, vec_out, a.V, col, d);
+    }
+  }
+}
+
+template <class E>
+cudaError_t launch_fwd(const KeepArgs& a, cudaStream_t st) {
+  // One row to a CTA while that fills the GPU twice; else its chunks over a
+  // cluster of up to eight CTAs, whose states meet in the first one's memory.
+  int parts = 1;
+  while (parts < kMaxCluster && a.T * parts < 2 * num_sms() && parts * kKeepWarps < a.chunks)
+    parts *= 2;
+  const size_t smem = static_cast<size_t>(a.chunks) * sizeof(float2);
+  cudaError_t e = cudaFuncSetAttribute(keep_logprob_kernel<E>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.T * parts));
+  cfg.blockDim = dim3(kKeepThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = parts;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, keep_logprob_kernel<E>, a);
+}
+
+template <class E>
+cudaError_t launch_bwd(const KeepArgs& a, cudaStream_t st) {
+  int parts = 1;
+  while (parts < 64 && a.T * parts < 4 * num_sms() && parts * kKeepWarps < a.chunks) parts *= 2;
+  keep_logprob_bwd_kernel<E><<<dim3(static_cast<unsigned>(a.T), parts), kKeepThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+int check(const void* logits, int64_t ld, int32_t dtype, int64_t T, int32_t V) {
+  if (T < 0 || T >= (int64_t(1) << 31) - 1 || V < 1 || V > (1 << 24)) return RZ_ERR_INVALID_ARG;
+  if (dtype != RZ_DTYPE_F32 && dtype != RZ_DTYPE_BF16 && dtype != RZ_DTYPE_F16)
+    return RZ_ERR_INVALID_ARG;
+  if (ld < V || (T > 0 && !logits)) return RZ_ERR_INVALID_ARG;
+  const uintptr_t size = dtype == RZ_DTYPE_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(logits) % size != 0) return RZ_ERR_UNSUPPORTED;
+  return RZ_OK;
+}
+
+}  // namespace
+}  // namespace rz
+
+using namespace rz;
+
+extern "C" {
+
+int rz_keep_logprob(const void* logits, int64_t ld, int32_t dtype, int64_t T, int32_t V,
+                    const uint32_t* keep, const float* temperature, const int32_t* tokens,
+                    float* logprob_out, float* lse_out, int32_t* err_flag, rz_stream_t stream) {
+  const int bad = check(logits, ld, dtype, T, V);
+  if (bad) return bad;
+  if (T > 0 && (!tokens || !logprob_out)) return RZ_ERR_INVALID_ARG;
+  if (T == 0) return RZ_OK;
+  if (!device_ok()) return RZ_ERR_UNSUPPORTED;
+  KeepArgs a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.keep = keep;
+  a.temperature = temperature;
+  a.tokens = tokens;
+  a.logprob = logprob_out;
+  a.lse = lse_out;
+  a.err = err_flag;
+  a.T = T;
+  a.V = V;
+  a.words = (V + 31) / 32;
+  a.chunks = (V + kKeepChunk - 1) / kKeepChunk;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope ps(RZ_PROF_LOGITS_ROWS, 1, st);
+  const cudaError_t e = dtype == RZ_DTYPE_F32    ? launch_fwd<float>(a, st)
+                        : dtype == RZ_DTYPE_BF16 ? launch_fwd<__nv_bfloat16>(a, st)
+                                                 : launch_fwd<__half>(a, st);
+  return e == cudaSuccess ? RZ_OK : RZ_ERR_CUDA;
+}
+
+int rz_keep_logprob_bwd(const void* logits, int64_t ld, int32_t dtype, int64_t T, int32_t V,
+                        const uint32_t* keep, const float* temperature, const int32_t* tokens,
+                        const float* lse, const float* dlogprob, void* dlogits, int64_t ldd,
+                        int32_t* err_flag, rz_stream_t stream) {
+  int bad = check(logits, ld, dtype, T, V);
+  if (!bad) bad = check(dlogits, ldd, dtype, T, V);
+  if (bad) return bad;
+  if (T > 0 && (!tokens || !lse || !dlogprob)) return RZ_ERR_INVALID_ARG;
+  if (logits == dlogits && ld != ldd && T > 1) return RZ_ERR_INVALID_ARG;
+  if (T == 0) return RZ_OK;
+  if (!device_ok()) return RZ_ERR_UNSUPPORTED;
+  KeepArgs a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.keep = keep;
+  a.temperature = temperature;
+  a.tokens = tokens;
+  a.lse_in = lse;
+  a.dlogprob = dlogprob;
+  a.dlogits = dlogits;
+  a.ldd = ldd;
+  a.err = err_flag;
+  a.T = T;
+  a.V = V;
+  a.words = (V + 31) / 32;
+  a.chunks = (V + kKeepChunk - 1) / kKeepChunk;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope ps(RZ_PROF_LOGITS_ROWS, 1, st);
+  const cudaError_t e = dtype == RZ_DTYPE_F32    ? launch_bwd<float>(a, st)
+                        : dtype == RZ_DTYPE_BF16 ? launch_bwd<__nv_bfloat16>(a, st)
+                                                 : launch_bwd<__half>(a, st);
+  return e == cudaSuccess ? RZ_OK : RZ_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,169 @@
+// rz_keep.cuh -- what the filtered sampler and the kept-set logprob share:
+// reading a row of logits of any of the three types, the row's temperature,
+// and the log-sum-exp over kept columns.
+//
+// The log-sum-exp runs over chunks of 2,048 columns.  A warp folds a chunk:
+// lane l holds columns 256 j + 8 l .. + 7 (j = 0..7) of it, takes the chunk's
+// maximum m over the kept ones and r = sum 2^((z - m) log2(e) / tau) over all of
+// them but one maximum (whose term is 1), columns not kept adding exactly 0;
+// the chunks' states are merged in a fixed order.  With that 1 left out,
+// log(1 + r) keeps its relative precision where one token has nearly all of
+// the probability.
+// The partition depends on nothing but the column, and every rounding is
+// spelled out, so sampler and learner give the same float for the same logits,
+// kept set and temperature, whatever the batch, grid or logit layout.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "rz_math.cuh"
+#include "rz_ptx.cuh"
+
+namespace rz {
+
+constexpr int kKeepChunk = 2048;
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+
+__device__ __forceinline__ void unpack8(const uint4* q, float (&v)[8], float) {
+  const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+}
+__device__ __forceinline__ void unpack8(const uint4* q, float (&v)[8], __nv_bfloat16) {
+  const uint32_t w[4] = {q->x, q->y, q->z, q->w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void unpack8(const uint4* q, float (&v)[8], __half) {
+  const uint32_t w[4] = {q->x, q->y, q->z, q->w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = *reinterpret_cast<const __half2*>(&w[i]);
+    v[2 * i] = __low2float(h);
+    v[2 * i + 1] = __high2float(h);
+  }
+}
+
+template <class E>
+__device__ __forceinline__ bool row_aligned(const E* row) {
+  return (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
+}
+
+// Columns col .. col+7 (col % 8 == 0); -inf past V.
+template <class E>
+__device__ __forceinline__ void load8(const E* row, bool vec, int V, int col, float (&v)[8]) {
+  if (vec && col + 8 <= V) {
+    uint4 q[sizeof(E) / 2];
+    const uint4* p = reinterpret_cast<const uint4*>(row + col);
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(E) / 2); ++i) q[i] = p[i];
+    unpack8(q, v, E());
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = col + i < V ? to_f32(row[col + i]) : -INFINITY;
+  }
+}
+
+// Row temperature: NaN if out of range (0 counts as 1; so does none).
+__device__ __forceinline__ float row_tau(const float* temperature, long long row) {
+  if (!temperature) return 1.f;
+  const float t = temperature[row];
+  if (t == 0.f) return 1.f;
+  return t >= 9.5367431640625e-07f && t <= 1048576.f ? t : __int_as_float(0x7fc00000);
+}
+
+// Fold of one chunk by one warp.  Kept: before(col) -> the 8 columns' bits that
+// may be kept (0: nothing is loaded), after(col, v, bits) -> those that are.
+template <class E, class Kept>
+__device__ __forceinline__ float2 keep_fold(const E* row, bool vec, int V, int chunk, float c,
+                                            const Kept& kept) {
+  const int col0 = chunk * kKeepChunk + 8 * (threadIdx.x & 31);
+  float v[8][8];
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int col = col0 + 256 * j;
+    uint32_t bits = col < V ? kept.before(col) : 0u;
+    if (bits) {
+      load8(row, vec, V, col, v[j]);
+      bits = kept.after(col, v[j], bits);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (!((bits >> i) & 1u)) v[j][i] = -INFINITY;
+      m = fmaxf(m, v[j][i]);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float ref = m == -INFINITY ? 0.f : m;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  int top = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = ex2_approx(__fmul_rn(__fsub_rn(v[j][i], ref), c));
+      const bool is_top = v[j][i] == m;
+      acc[i & 3] = __fadd_rn(acc[i & 3], is_top ? 0.f : t);
+      top += is_top;
+    }
+  float r = __fadd_rn(__fadd_rn(acc[0], acc[1]), __fadd_rn(acc[2], acc[3]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, o));
+    top += __shfl_xor_sync(0xffffffffu, top, o);
+  }
+  // an empty chunk: 0 (NaN if it holds NaNs)
+  return make_float2(m, m == -INFINITY ? r : __fadd_rn(r, static_cast<float>(top - 1)));
+}
+
+// Merge of the chunks' states by one warp: max, then each lane adds every
+// 32nd state in order, then a butterfly.
+__device__ __forceinline__ float2 keep_merge(const float2* st, int n, float c) {
+  const int lane = threadIdx.x & 31;
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, st[i].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float ref = M == -INFINITY ? 0.f : M;
+  float r = 0.f;
+  int top = 0;
+  for (int i = lane; i < n; i += 32) {
+    const float2 x = st[i];
+    if (x.x == -INFINITY || x.x == M) {
+      r = __fadd_rn(r, x.y);
+      top += x.x == M;
+    } else {
+      const float f = ex2_approx(__fmul_rn(__fsub_rn(x.x, ref), c));
+      r = __fadd_rn(r, __fmul_rn(__fadd_rn(x.y, 1.f), f));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, o));
+    top += __shfl_xor_sync(0xffffffffu, top, o);
+  }
+  return make_float2(M, M == -INFINITY ? r : __fadd_rn(r, static_cast<float>(top - 1)));
+}
+
+// log2(e) / tau, the log-probability of logit za and the log-sum-exp.
+__device__ __forceinline__ float keep_scale(float tau) { return __fdiv_rn(kLog2e, tau); }
+__device__ __forceinline__ float keep_logprob_of(float za, float2 state, float tau) {
+  return __fsub_rn(__fdiv_rn(__fsub_rn(za, state.x), tau), log1pf(state.y));
+}
+__device__ __forceinline__ float keep_lse_of(float2 state, float tau) {
+  return __fadd_rn(__fdiv_rn(state.x, tau), log1pf(state.y));
+}
+
+}  // namespace rz

@@ -317,7 +317,7 @@ size_t rz_workspace_size(int op, int64_t T, int32_t d, int32_t V, int32_t B) {
     case RZ_OP_IS_LOSS: return is_loss_ws_bytes(B);
     case RZ_OP_SAMPLE:
       return sample_layout(T, V > 0 ? V : 1).total + decode_bytes(T, V > 0 ? V : 1);
-    case RZ_OP_GROUP_DECODE_ATTN: return 0;
+    case RZ_OP_GROUP_DECODE_ATTN: return group_decode_attn_ws_bytes(T, B, V, d);
     default: return 0;
   }
 }

@@ -200,4 +200,7 @@ cudaError_t launch_logits_rows(uint16_t* logits, int64_t T, int V, const int32_t
                                const uint8_t* mask, int B, float* logprob, int* err,
                                cudaStream_t st);
 
+// ---- group decode attention (rz_attn.cu)
+size_t group_decode_attn_ws_bytes(int64_t B, int32_t P, int32_t Hq, int32_t D);
+
 }  // namespace rz

@@ -449,7 +449,9 @@ RZ_API int rz_page_tables(const int32_t* lens, const int32_t* new_lens, int32_t 
  * rounded to the inputs' type as the second product's operand.
  * Requires: Hq % Hkv == 0, Hq / Hkv <= 128, D % 8 == 0, 8 <= D <= 128, and
  * 16-byte alignment of q, k_cache, v_cache, out and all strides
- * (RZ_ERR_UNSUPPORTED otherwise); B, P >= 0.
+ * (RZ_ERR_UNSUPPORTED otherwise), q's strides positive; B, P >= 0.  Page
+ * sizes 8, 16, 32, 64 and multiples of 128 are read page by page through
+ * tensor maps, all others row by row.
  * Lengths past a row's width or negative are cut, page ids outside
  * [0, n_pages) are skipped, a cu_group that is not 0 <= cu[0] <= ... <= B is
  * cut to it: RZ_DEVERR_PAGES / RZ_DEVERR_CU_SEQLENS, no access leaves the

@@ -24,10 +24,11 @@
 //              reference m moves only when a row's maximum has grown by more
 //              than 8 (a factor 2^8, far inside fp32's and fp16's range), so
 //              O is rarely rescaled.  Warps without rows only keep step.
-//   warps 4-7  loads: 16-byte asynchronous copies, swizzled by address, which
-//              take any page size and stride and zero what lies past the
-//              length; the reads of six to seven tiles a CTA are in flight.
-//   warp 8     TMEM owner and MMA issuer: S of tile j+1 before P V of tile j.
+//   warp 4     TMA: query rows, and K and V of full tiles page by page (page
+//              sizes 8, 16, 32, 64 and multiples of 128), one lane a page.
+//   warps 5-8  16-byte asynchronous copies for every other tile, which zero
+//              what is not there: 0 times a stray NaN of V would be NaN.
+//   warp 9     TMEM owner and MMA issuer: S of tile j+1 before P V of tile j.
 // A tile's K and V are 64 KB at 128 columns; at its share of the memory an SM
 // takes 2,800 clocks for that, while the two products take 1,100 and the
 // softmax of a full warp about 1,000: the memory is what bounds it, whatever
@@ -47,11 +48,10 @@ namespace {
 constexpr int kTile = 128;      // tokens per tile, query rows per item
 constexpr int kMaxD = 128;
 constexpr int kMaxCtas = 152;   // persistent CTAs at most (workspace size)
-constexpr int kSoftWarps = 4, kLoadWarps = 4;
-constexpr int kMmaWarp = kSoftWarps + kLoadWarps;
+constexpr int kSoftWarps = 4, kTmaWarp = 4, kCopyWarp0 = 5, kMmaWarp = 9;
+constexpr int kCopyWarps = kMmaWarp - kCopyWarp0;
 constexpr int kAttnThreads = 32 * (kMmaWarp + 1);
 constexpr int kSlots = 5;       // ring of K and V tiles
-constexpr int kLag = 3;         // fills issued but not yet announced
 constexpr uint32_t kHalf = kTile * 128;       // 128 rows x 64 columns, 16 KB
 constexpr uint32_t kSlotBytes = 2 * kHalf;    // 32 KB
 constexpr int kMaskRing = 8;
@@ -62,6 +62,9 @@ constexpr uint32_t kAttnSmem = kSmemCtl + 1024 + 1024;     // control block, ali
 // TMEM columns: O, two S, two P
 constexpr uint32_t kColO = 0, kColS = 128, kColP = 384;
 constexpr float kGrow = 8.f;
+// What beginning and ending an item costs, in tiles: the line that is cut
+// into runs has this many empty places before each item's tiles.
+constexpr int kItemCost = 1;
 
 struct AttnArgs {
   const void *q, *k, *v;
@@ -72,6 +75,8 @@ struct AttnArgs {
   int* err;
   float scale;  // times log2 e
   int n_pages, page, prefix_width, P, width, B, Hq, Hkv, D, rep, ctas;
+  int row_tile;       // query rows per prompt item: whole requests, at most 128
+  int paged_tma;      // pages and tiles fit each other: full tiles come by TMA
   // workspace
   long long* starts;  // [P + B + 1] first tile of each entry
   int32_t* clen;      // [P + B] clean lengths
@@ -150,10 +155,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs a) {
   const int per = (E + kPlanThreads - 1) / kPlanThreads;
   const int e0 = min(threadIdx.x * per, E), e1 = min(e0 + per, E);
   const auto tiles = [&](int e, int len) -> long long {
-    long long t = static_cast<long long>((len + kTile - 1) / kTile) * a.Hkv;
+    if (len == 0) return 0;
+    long long t = static_cast<long long>((len + kTile - 1) / kTile + kItemCost) * a.Hkv;
     if (e < a.P) {
       const long long rows = static_cast<long long>(a.cu[e + 1] - a.cu[e]) * a.rep;
-      t *= (rows + kTile - 1) / kTile;
+      t *= (rows + a.row_tile - 1) / a.row_tile;
     }
     return t;
   };
@@ -178,7 +184,7 @@ struct Walk {
   long long per;
   int e;              // entry: prompt e < P, request e - P
   // the part at x
-  int head, row_tile, n_tiles, t0, t1, len, rows;
+  int head, row_tile, n_tiles, t0, t1, len, rows, taken;
   bool first;         // begins at the item's first tile
 
   __device__ __forceinline__ void init(const AttnArgs& a, int cta) {
@@ -197,36 +203,45 @@ struct Walk {
     }
     e = lo;
   }
-  // Describe the part at x; false at the end.
+  // Describe the next part with a tile from x on; false at the end.
   __device__ __forceinline__ bool part(const AttnArgs& a) {
-    if (x >= end) return false;
+    while (x < end) {
+      describe(a);
+      if (t0 < t1) return true;
+      next();
+    }
+    return false;
+  }
+  __device__ __forceinline__ void describe(const AttnArgs& a) {
     while (a.starts[e + 1] <= x) ++e;
     len = a.clen[e];
     n_tiles = (len + kTile - 1) / kTile;
+    const int places = n_tiles + kItemCost;
     const long long at = x - a.starts[e];
-    const long long item = at / n_tiles;
-    t0 = static_cast<int>(at - item * n_tiles);
-    const long long left = end - x;
-    t1 = left < n_tiles - t0 ? t0 + static_cast<int>(left) : n_tiles;
+    const long long item = at / places;
+    const int p0 = static_cast<int>(at - item * places);
+    const int p1 = end - x < places - p0 ? p0 + static_cast<int>(end - x) : places;
+    taken = p1 - p0;
+    t0 = max(p0 - kItemCost, 0);
+    t1 = max(p1 - kItemCost, 0);  // t0 = t1: the run ends before the first tile
     first = t0 == 0;
     if (e < a.P) {
       const int group_rows = (a.cu[e + 1] - a.cu[e]) * a.rep;
-      const int row_tiles = (group_rows + kTile - 1) / kTile;
+      const int row_tiles = (group_rows + a.row_tile - 1) / a.row_tile;
       head = static_cast<int>(item / row_tiles);
       row_tile = static_cast<int>(item) - head * row_tiles;
-      rows = min(kTile, group_rows - row_tile * kTile);
+      rows = min(a.row_tile, group_rows - row_tile * a.row_tile);
     } else {
       head = static_cast<int>(item);
       row_tile = 0;
       rows = a.rep;
     }
-    return true;
   }
-  __device__ __forceinline__ void next() { x += t1 - t0; }
+  __device__ __forceinline__ void next() { x += taken; }
   // request and query head of row r of the part
   __device__ __forceinline__ void row(const AttnArgs& a, int r, int& b, int& h) const {
     if (e < a.P) {
-      const int i = row_tile * kTile + r;
+      const int i = row_tile * a.row_tile + r;
       b = a.cu[e] + i / a.rep;
       h = head * a.rep + i % a.rep;
     } else {
@@ -237,11 +252,12 @@ struct Walk {
 };
 
 struct AttnCtl {
-  uint64_t kv_full[kSlots], kv_empty[kSlots];
-  uint64_t q_empty[2], s_full[2], s_empty[2], p_full[2], pv_done[2], o_free, drain;
+  uint64_t kv_full[kSlots], kv_empty[kSlots], go[kCopyWarps];
+  uint64_t q_full[2], q_empty[2], s_full[2], s_empty[2], p_full[2], pv_done[2], o_free, drain;
   uint32_t mask[kMaskRing][4];
   uint32_t tmem;
   int abort;
+  int tma_fill[kSlots], tma_q[2];  // last fill, item that a TMA copy was issued for; -1
 };
 static_assert(sizeof(AttnCtl) <= 1024, "control block");
 
@@ -261,26 +277,46 @@ __device__ __forceinline__ bool warp_wait(AttnCtl* c, uint64_t* bar, uint32_t pa
   return ok != 0;
 }
 
-// A 128 x D tile of rows into its swizzled place: `row` is the start of this
-// lane's row (row 32 w + lane of the tile), ok whether it is read or zeroed.
-__device__ __forceinline__ void load_rows(uint32_t dst, const uint8_t* row, bool ok, int rows,
-                                          int warp, int chunks) {
+// 32 rows of a tile into their swizzled place: `row` is the start of this
+// lane's row (row 32 w + lane of the tile), `fill` the rows that are written,
+// `read` those of them that are read and not zeroed.
+// kLanes lanes take one row's 16-byte chunks.  The loop is unrolled so that
+// the exchanges of row addresses overlap: one by one they take 106 clocks an
+// iteration.
+template <int kLanes>
+__device__ __forceinline__ void load_rows_n(uint32_t dst, const uint8_t* row, uint32_t read,
+                                            uint32_t fill, int w, int chunks) {
   const int lane = threadIdx.x & 31;
-  const uint32_t valid = __ballot_sync(0xffffffffu, ok);
-  const int per_row = chunks <= 8 ? 8 : 16;  // lanes of a row
-  const int step = 32 / per_row;
-  const int c = lane % per_row, sub = lane / per_row;
-  const int limit = min(32, rows - 32 * warp);
-  for (int r0 = 0; r0 < limit; r0 += step) {
-    const int r = r0 + sub;
+  constexpr int kStep = 32 / kLanes;
+  const int c = lane % kLanes, sub = lane / kLanes;
+  const bool mine = c < chunks;
+  const uint32_t base = dst + (c >> 3) * kHalf + (32 * w + sub) * 128;
+#pragma unroll
+  for (int i = 0; i < kLanes; ++i) {
+    const int r = sub + kStep * i;
     const uint8_t* p = reinterpret_cast<const uint8_t*>(
         __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r));
-    if (c < chunks) {
-      const int tr = 32 * warp + r;
-      const uint32_t at = dst + (c >> 3) * kHalf + tr * 128 + (((c & 7) ^ (tr & 7)) << 4);
-      cp_async16(at, p + 16 * c, (valid >> r) & 1u ? 16u : 0u);
-    }
+    if (mine && (fill >> r) & 1u)
+      cp_async16(base + kStep * i * 128 + (((c & 7) ^ (r & 7)) << 4), p + 16 * c,
+                 (read >> r) & 1u ? 16u : 0u);
   }
+}
+
+// Whether a tile of the part comes by TMA: every token there and every page
+// of it in the pool (pg: this lane's page, of the tile's first `n`).
+__device__ __forceinline__ bool by_tma(const AttnArgs& a, const Walk& w, const int32_t* tab, int t,
+                                       int& pg, int& n) {
+  if (!a.paged_tma || (t + 1) * static_cast<long long>(kTile) > w.len) return false;
+  n = a.page < kTile ? kTile / a.page : 1;
+  const int first = static_cast<int>(static_cast<long long>(t) * kTile / a.page);
+  const int lane = threadIdx.x & 31;
+  pg = lane < n ? tab[first + lane] : 0;
+  return __all_sync(0xffffffffu, pg >= 0 && pg < a.n_pages);
+}
+
+__device__ __forceinline__ const int32_t* page_row(const AttnArgs& a, const Walk& w) {
+  return w.e < a.P ? a.prefix_table + static_cast<long long>(w.e) * a.prefix_width
+                   : a.table + static_cast<long long>(w.e - a.P) * a.width;
 }
 
 template <class E>
@@ -294,23 +330,75 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   return pack_f16x2(lo, hi);
 }
 
-// Scores as the softmax takes them: sign (a negative scale), no scale at all,
-// -inf at tokens that are not there.
-__device__ __forceinline__ void adjust(uint32_t (&s)[32], uint32_t bits, bool all, bool flip,
-                                       bool zero) {
-  if (flip || zero) {
+// What the softmax does to raw scores on the rare paths: turn the sign (a
+// negative scale), drop them (no scale), -inf at tokens that are not there.
+__device__ __forceinline__ void adjust(uint32_t (&s)[32], uint32_t bits, bool flip, bool zero) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s[i] = zero ? 0u : s[i] ^ 0x80000000u;
-  }
-  if (!all) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (!((bits >> i) & 1u)) s[i] = 0xff800000u;
+  for (int i = 0; i < 32; ++i) {
+    s[i] = zero ? 0u : (flip ? s[i] ^ 0x80000000u : s[i]);
+    if (!((bits >> i) & 1u)) s[i] = 0xff800000u;
   }
 }
 
+// One half (64 columns) of a thread's scores, by how much of it is there.
+// The selects of a partly filled half would double the instructions of a full
+// one, so the three have code of their own (the choice is the warp's).
+enum HalfKind { kHalfFull, kHalfPart, kHalfNone };
+__device__ __forceinline__ HalfKind half_kind(uint32_t b0, uint32_t b1, bool general) {
+  if ((b0 | b1) == 0u) return kHalfNone;
+  return (b0 & b1) == 0xffffffffu && !general ? kHalfFull : kHalfPart;
+}
+
+template <bool kPart>
+__device__ __forceinline__ float half_max(uint32_t sc, uint32_t b0, uint32_t b1, bool flip,
+                                          bool zero) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  uint32_t s[2][32];
+  tmem_ld32(sc, s[0]);
+  tmem_ld32(sc + 32, s[1]);
+  tmem_ld_wait();
+  if (kPart) {
+    adjust(s[0], b0, flip, zero);
+    adjust(s[1], b1, flip, zero);
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    mx[i & 1] = fmaxf(mx[i & 1], __uint_as_float(s[0][i]));
+    mx[2 + (i & 1)] = fmaxf(mx[2 + (i & 1)], __uint_as_float(s[1][i]));
+  }
+  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+
+// The terms 2^(sl s - ref) into P, in 16 bits; returns their sum.
+template <class E, bool kPart>
+__device__ __forceinline__ float half_terms(uint32_t sc, uint32_t pc, uint32_t b0, uint32_t b1,
+                                            bool flip, bool zero, float sl, float ref) {
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  uint32_t s[2][32], pk[32];
+  tmem_ld32(sc, s[0]);
+  tmem_ld32(sc + 32, s[1]);
+  tmem_ld_wait();
+  if (kPart) {
+    adjust(s[0], b0, flip, zero);
+    adjust(s[1], b1, flip, zero);
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float p0 = ex2_approx(fmaf(__uint_as_float(s[i >> 4][2 * (i & 15)]), sl, -ref));
+    const float p1 = ex2_approx(fmaf(__uint_as_float(s[i >> 4][2 * (i & 15) + 1]), sl, -ref));
+    acc[i & 3] += p0 + p1;
+    pk[i] = pack2<E>(p0, p1);
+  }
+  tmem_st32(pc, pk);
+  return (acc[0] + acc[1]) + (acc[2] + acc[3]);
+}
+
 template <class E>
-__global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v,
+                const __grid_constant__ CUtensorMap tm_q_group,
+                const __grid_constant__ CUtensorMap tm_q_own) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -320,10 +408,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const AttnArgs a)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&ctl->kv_full[s], kLoadWarps);
+      mbar_init(&ctl->kv_full[s], 1);
       mbar_init(&ctl->kv_empty[s], 1);
+      ctl->tma_fill[s] = -1;
     }
+    for (int i = 0; i < kCopyWarps; ++i) mbar_init(&ctl->go[i], 1);
+    ctl->tma_q[0] = ctl->tma_q[1] = -1;
     for (int b = 0; b < 2; ++b) {
+      mbar_init(&ctl->q_full[b], 1);
       mbar_init(&ctl->q_empty[b], 1);
       mbar_init(&ctl->s_full[b], 1);
       mbar_init(&ctl->s_empty[b], kSoftWarps);
@@ -355,100 +447,130 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const AttnArgs a)
 
   Walk w;
   w.init(a, blockIdx.x);
-  const int chunks = a.D / 8;
 
-  if (warp >= kSoftWarps && warp < kMmaWarp) {
-    // ---------------------------------------------------------------- loads
-    const int lw = warp - kSoftWarps;
-    int fill = 0;       // K and V tiles issued
-    int told = 0;       // ... and announced
-    bool ok = true;
-    int bad = 0;
-    int item = 0;       // parts begun
+  // Fill f of the ring is K of tile f / 2, then its V.  The TMA warp claims
+  // every slot in order; a fill that is not its own it hands to copy warp
+  // f mod 4 (at most two such ahead of what that warp has done, as the ring
+  // is shorter than eight).
+  const uint32_t halves = a.D > 64 ? 2u : 1u;
+  if (warp == kTmaWarp) {
+    // ---------------------------------------------------------------- TMA
     uint32_t tile = 0;
-    // Announce fills up to `upto`; their copies have been waited for.
-    const auto announce = [&](int upto) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0)
-        for (; told < upto; ++told) mbar_arrive(&ctl->kv_full[told % kSlots]);
-      told = upto;
-    };
-    // Wait until the products have released a buffer.  If that takes waiting,
-    // everything issued is announced first: it is what they wait for.
-    const auto wait_free = [&](uint64_t* bar, uint32_t ph) {
-      if (!__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), ph))) {
-        cp_async_wait<0>();
-        announce(fill);
-        ok = warp_wait(ctl, bar, ph, a.err);
-      }
-      return ok;
-    };
-    const auto claim = [&]() {  // the next slot of the ring
-      return fill < kSlots || wait_free(&ctl->kv_empty[fill % kSlots],
-                                        static_cast<uint32_t>((fill / kSlots + 1) & 1));
-    };
-    const auto issued = [&]() {
-      cp_async_commit();
-      ++fill;
-      if (fill - told > kLag) {
-        cp_async_wait<kLag>();
-        announce(fill - kLag);
-      }
-    };
+    int item = 0;
+    bool ok = true;
     while (ok && w.part(a)) {
-      const int32_t* tab = w.e < a.P
-                               ? a.prefix_table + static_cast<long long>(w.e) * a.prefix_width
-                               : a.table + static_cast<long long>(w.e - a.P) * a.width;
-      for (int t = w.t0; t < w.t1; ++t, ++tile) {
-        // this lane's token of the tile
-        const long long tok = static_cast<long long>(t) * kTile + 32 * lw + lane;
-        bool valid = tok < w.len;
-        long long ko = 0, vo = 0;
-        if (valid) {
-          const long long j = tok / a.page;
-          const int pg = tab[j];
-          if (pg >= 0 && pg < a.n_pages) {
-            const long long off = tok - j * a.page;
-            ko = pg * a.ks[0] + off * a.ks[1] + w.head * a.ks[2];
-            vo = pg * a.vs[0] + off * a.vs[1] + w.head * a.vs[2];
-          } else {
-            valid = false;
-            bad = RZ_DEVERR_PAGES;
+      const int32_t* tab = page_row(a, w);
+      // the part's query rows: whole requests' heads of this KV head
+      const int qb = item & 1;
+      if (item >= 2 && !(ok = warp_wait(ctl, &ctl->q_empty[qb], (item / 2 + 1) & 1u, a.err))) break;
+      if (lane == 0) {
+        const bool group = w.e < a.P;
+        const uint32_t rows = group ? a.row_tile : a.rep;
+        mbar_arrive_expect_tx(&ctl->q_full[qb], rows * 128 * halves);
+        ctl->tma_q[qb] = item;
+        const int b = group ? a.cu[w.e] + w.row_tile * (a.row_tile / a.rep) : w.e - a.P;
+        for (uint32_t i = 0; i < halves; ++i)
+          tma_load_3d(smem + kSmemQ + qb * kSlotBytes + i * kHalf, group ? &tm_q_group : &tm_q_own,
+                      &ctl->q_full[qb], 64 * i, w.head * a.rep, b);
+      }
+      ++item;
+      for (int t = w.t0; ok && t < w.t1; ++t, ++tile) {
+        int pg = 0, n = 0;
+        const bool mine = by_tma(a, w, tab, t, pg, n);
+        const int row = static_cast<int>(static_cast<long long>(t) * kTile % a.page);
+        for (uint32_t kv = 0; kv < 2; ++kv) {
+          const uint32_t f = 2 * tile + kv, slot = f % kSlots;
+          if (f >= kSlots &&
+              !(ok = warp_wait(ctl, &ctl->kv_empty[slot], (f / kSlots + 1) & 1u, a.err)))
+            break;
+          if (!mine) {
+            if (lane == 0) mbar_arrive(&ctl->go[f % kCopyWarps]);
+            continue;
           }
+          if (kv == 0 && lane < 4) ctl->mask[tile % kMaskRing][lane] = 0xffffffffu;
+          __syncwarp();
+          if (lane == 0) {
+            ctl->tma_fill[slot] = static_cast<int>(f);
+            mbar_arrive_expect_tx(&ctl->kv_full[slot], halves * kHalf);
+          }
+          __syncwarp();
+          uint8_t* dst = smem + kSmemKv + slot * kSlotBytes;
+          if (lane < n)
+            for (uint32_t i = 0; i < halves; ++i)
+              tma_load_4d(dst + i * kHalf + lane * a.page * 128, kv == 0 ? &tm_k : &tm_v,
+                          &ctl->kv_full[slot], 64 * i, w.head, row, pg);
         }
-        const uint32_t bits = __ballot_sync(0xffffffffu, valid);
-        if (!claim()) break;
-        if (t == w.t0) {
-          // the part's query rows ride with its first K tile
-          const int qb = item & 1;
-          if (item >= 2) {
-            const uint32_t ph = static_cast<uint32_t>((item / 2 + 1) & 1);
-            if (!wait_free(&ctl->q_empty[qb], ph)) break;
-          }
-          const int r = 32 * lw + lane;
-          const uint8_t* qrow = static_cast<const uint8_t*>(a.q);
-          if (r < w.rows) {
-            int b, h;
-            w.row(a, r, b, h);
-            qrow += 2 * (b * a.qs[0] + h * a.qs[1]);
-          }
-          load_rows(base + kSmemQ + qb * kSlotBytes, qrow, r < w.rows, w.rows, lw, chunks);
-          ++item;
-        }
-        if (lane == 0) ctl->mask[tile % kMaskRing][lw] = bits;
-        load_rows(base + kSmemKv + (fill % kSlots) * kSlotBytes,
-                  static_cast<const uint8_t*>(a.k) + 2 * ko, valid, kTile, lw, chunks);
-        issued();
-        if (!claim()) break;
-        load_rows(base + kSmemKv + (fill % kSlots) * kSlotBytes,
-                  static_cast<const uint8_t*>(a.v) + 2 * vo, valid, kTile, lw, chunks);
-        issued();
       }
       w.next();
     }
-    cp_async_wait<0>();
-    announce(fill);
+  } else if (warp >= kCopyWarp0 && warp < kMmaWarp) {
+    // ---------------------------------------------------------------- copies
+    // Tiles with fewer than 128 tokens or a page outside the pool, and all
+    // tiles where the page size does not fit: 16-byte copies that zero what
+    // is not there.
+    const uint32_t cw = warp - kCopyWarp0;
+    const bool is_k = (cw & 1u) == 0;
+    const int chunks = a.D / 8;
+    uint32_t tile = 0, done = 0;
+    bool ok = true;
+    int bad = 0;
+    while (ok && w.part(a)) {
+      const int32_t* tab = page_row(a, w);
+      for (int t = w.t0; ok && t < w.t1; ++t, ++tile) {
+        if ((tile & 1u) != (cw >> 1)) continue;
+        int unused_pg, unused_n;
+        if (by_tma(a, w, tab, t, unused_pg, unused_n)) continue;
+        const uint32_t slot = (2 * tile + (cw & 1u)) % kSlots;
+        if (!(ok = warp_wait(ctl, &ctl->go[cw], done & 1u, a.err))) break;
+        ++done;
+        const uint8_t* src = static_cast<const uint8_t*>(is_k ? a.k : a.v);
+        const long long* st = is_k ? a.ks : a.vs;
+        const uint32_t dst = base + kSmemKv + slot * kSlotBytes;
+        // K: the tokens there are (the other scores are never looked at).  V:
+        // up to the product's depth, zeros where there is no token, as 0
+        // times a stray NaN would be NaN.
+        const uint32_t here = static_cast<uint32_t>(min(w.len - t * kTile, kTile));
+        const uint32_t deep = is_k ? here : (here + 15) / 16 * 16;
+        int pg[4];
+        uint32_t off[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {  // the page ids' loads overlap
+          const uint32_t i = 32 * g + lane;
+          pg[g] = -1;
+          off[g] = 0;
+          if (i < here) {
+            const uint32_t tok = static_cast<uint32_t>(t) * kTile + i;
+            const uint32_t j = tok / static_cast<uint32_t>(a.page);
+            off[g] = tok - j * static_cast<uint32_t>(a.page);
+            pg[g] = tab[j];
+            if (pg[g] < 0 || pg[g] >= a.n_pages) {
+              pg[g] = -1;
+              bad = RZ_DEVERR_PAGES;
+            }
+          }
+        }
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          const int page = g == 0 ? pg[0] : g == 1 ? pg[1] : g == 2 ? pg[2] : pg[3];
+          const uint32_t o = g == 0 ? off[0] : g == 1 ? off[1] : g == 2 ? off[2] : off[3];
+          const uint32_t read = __ballot_sync(0xffffffffu, page >= 0);
+          if (is_k && lane == 0) ctl->mask[tile % kMaskRing][g] = read;
+          const uint32_t fill = __ballot_sync(0xffffffffu, 32u * g + lane < deep);
+          if (fill == 0) continue;
+          const uint8_t* row = src;
+          if (page >= 0)
+            row += 2 * (page * st[0] + static_cast<long long>(o) * st[1] + w.head * st[2]);
+          if (chunks > 8) load_rows_n<16>(dst, row, read, fill, g, chunks);
+          else load_rows_n<8>(dst, row, read, fill, g, chunks);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->kv_full[slot]);
+      }
+      w.next();
+    }
     if (bad && a.err) atomicOr(a.err, bad);
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- products
@@ -456,7 +578,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const AttnArgs a)
       const uint32_t fmt = sizeof(E) == 2 && std::is_same<E, __nv_bfloat16>::value
                                ? (1u << 7) | (1u << 10) : 0u;
       const uint32_t depth = (a.D + 15) / 16;
-      const uint32_t idesc_s = (1u << 4) | fmt | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
+      const uint32_t idesc_s = (1u << 4) | fmt | ((kTile >> 4) << 24);  // and N / 8 << 17
       const uint32_t idesc_o = (1u << 4) | fmt | (1u << 16) | ((2 * depth) << 17) |
                                ((kTile >> 4) << 24);
       const volatile int* abort = const_cast<volatile int*>(&ctl->abort);
@@ -464,7 +586,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const AttnArgs a)
       uint32_t tile = 0;   // S issued
       int item = 0, o_items = 0;
       bool pend = false, pend_first = false;  // the tile whose P V is due
-      const auto pv = [&](uint32_t j, bool fresh) {
+      int pend_k = 0;                         // its tokens / 16
+      const auto pv = [&](uint32_t j, bool fresh, int steps) {
         const uint32_t b = j & 1u, use = (j >> 1) & 1u;
         const uint32_t f = 2 * j + 1;
         const uint32_t slot = f % kSlots;
@@ -478,8 +601,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const AttnArgs a)
         }
         tc_fence_after();
         const uint32_t v = base + kSmemKv + slot * kSlotBytes;
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
+        for (int k = 0; k < steps; ++k)
           umma_f16_ts(tmem + kColO, tmem + kColP + 64 * b + 8 * k,
                       sdesc_sw128(v + 2048u * k, kHalf, 1024u), idesc_o,
                       (fresh && k == 0) ? 0u : 1u);
@@ -489,6 +611,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const AttnArgs a)
       };
       while (ok && w.part(a)) {
         const uint32_t q = base + kSmemQ + (item & 1) * kSlotBytes;
+        if (!mbar_wait(&ctl->q_full[item & 1], (item >> 1) & 1u, abort, kWaitLimitNs)) {
+          ok = false;
+          break;
+        }
         for (int t = w.t0; t < w.t1; ++t, ++tile) {
           const uint32_t b = tile & 1u, use = (tile >> 1) & 1u;
           const uint32_t f = 2 * tile;
@@ -499,26 +625,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const AttnArgs a)
             break;
           }
           tc_fence_after();
+          const int n16 = (min(w.len - t * kTile, kTile) + 15) / 16;  // tokens / 16
+          const uint32_t idesc = idesc_s | (static_cast<uint32_t>(2 * n16) << 17);
           const uint32_t k0 = base + kSmemKv + slot * kSlotBytes;
           for (uint32_t k = 0; k < depth; ++k) {
             const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32u;
             umma_bf16(tmem + kColS + 128 * b, sdesc_sw128(q + off, 16u, 1024u),
-                      sdesc_sw128(k0 + off, 16u, 1024u), idesc_s, k > 0 ? 1u : 0u);
+                      sdesc_sw128(k0 + off, 16u, 1024u), idesc, k > 0 ? 1u : 0u);
           }
           umma_commit(&ctl->kv_empty[slot]);
           umma_commit(&ctl->s_full[b]);
           if (t == w.t1 - 1) umma_commit(&ctl->q_empty[item & 1]);
-          if (pend && !pv(tile - 1, pend_first)) {
+          if (pend && !pv(tile - 1, pend_first, pend_k)) {
             ok = false;
             break;
           }
           pend = true;
           pend_first = t == w.t0;
+          pend_k = n16;
         }
         ++item;
         w.next();
       }
-      if (ok && pend) ok = pv(tile - 1, pend_first);
+      if (ok && pend) ok = pv(tile - 1, pend_first, pend_k);
       if (!ok) attn_abort(ctl, a.err);
       // no MMA is in flight when TMEM is freed
       umma_commit(&ctl->drain);
@@ -544,25 +673,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const AttnArgs a)
         for (int i = 0; i < 4; ++i) bits[i] = ctl->mask[tile % kMaskRing][i];
         if (live) {
           const uint32_t sc = lanes + kColS + 128 * b;
-          const bool all = (bits[0] & bits[1] & bits[2] & bits[3]) == 0xffffffffu;
-          // two passes over S, 64 columns in registers at a time: the
-          // maximum, then the terms
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t s[2][32];
-            tmem_ld32(sc + 64 * half, s[0]);
-            tmem_ld32(sc + 64 * half + 32, s[1]);
-            tmem_ld_wait();
-            adjust(s[0], bits[2 * half], all, flip, zero);
-            adjust(s[1], bits[2 * half + 1], all, flip, zero);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              mx[i & 1] = fmaxf(mx[i & 1], __uint_as_float(s[0][i]));
-              mx[2 + (i & 1)] = fmaxf(mx[2 + (i & 1)], __uint_as_float(s[1][i]));
-            }
-          }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+          const bool general = flip || zero;
+          const HalfKind h0 = half_kind(bits[0], bits[1], general);
+          const HalfKind h1 = half_kind(bits[2], bits[3], general);
+          float top = -INFINITY;
+          if (h0 == kHalfFull) top = half_max<false>(sc, 0u, 0u, false, false);
+          else if (h0 == kHalfPart) top = half_max<true>(sc, bits[0], bits[1], flip, zero);
+          if (h1 == kHalfFull) top = fmaxf(top, half_max<false>(sc + 64, 0u, 0u, false, false));
+          else if (h1 == kHalfPart)
+            top = fmaxf(top, half_max<true>(sc + 64, bits[2], bits[3], flip, zero));
+          top *= sl;
           const bool grow = top > m + kGrow || (m == -INFINITY && top > m);
           if (t > w.t0 && __any_sync(0xffffffffu, grow)) {
             // O of the tiles before moves to the new reference
@@ -583,31 +703,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const AttnArgs a)
           }
           if (grow) m = top;
           const float ref = m == -INFINITY ? 0.f : m;
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t s[2][32], pk[32];
-            tmem_ld32(sc + 64 * half, s[0]);
-            tmem_ld32(sc + 64 * half + 32, s[1]);
-            tmem_ld_wait();
-            if (half == 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&ctl->s_empty[b]);
-            }
-            adjust(s[0], bits[2 * half], all, flip, zero);
-            adjust(s[1], bits[2 * half + 1], all, flip, zero);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float p0 = ex2_approx(fmaf(__uint_as_float(s[i >> 4][2 * (i & 15)]), sl, -ref));
-              const float p1 =
-                  ex2_approx(fmaf(__uint_as_float(s[i >> 4][2 * (i & 15) + 1]), sl, -ref));
-              acc[i & 3] += p0 + p1;
-              pk[i] = pack2<E>(p0, p1);
-            }
-            tmem_st32(lanes + kColP + 64 * b + 32 * half, pk);
-          }
-          l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+          const uint32_t pc = lanes + kColP + 64 * b;
+          // a half without a token is no part of the second product, unless
+          // a page inside the length is missing: then its terms are zeros
+          const uint32_t here = static_cast<uint32_t>(w.len - t * kTile);
+          const auto terms = [&](HalfKind kind, uint32_t off, uint32_t b0, uint32_t b1) {
+            if (kind == kHalfFull)
+              l += half_terms<E, false>(sc + off, pc + off / 2, 0u, 0u, false, false, sl, ref);
+            else if (kind == kHalfPart || here > off)
+              l += half_terms<E, true>(sc + off, pc + off / 2, b0, b1, flip, zero, sl, ref);
+          };
+          terms(h0, 0, bits[0], bits[1]);
+          terms(h1, 64, bits[2], bits[3]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->s_empty[b]);
           tmem_st_wait();
         } else {
           tc_fence_before();
@@ -651,6 +761,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const AttnArgs a)
   }
   __syncwarp();
   tc_fence_before();
+  __syncthreads();
+  if (*const_cast<volatile int*>(&ctl->abort) && threadIdx.x == 0) {
+    // (after a wait that gave up) no copy lands once the CTA is gone
+    const auto settle = [](uint64_t* bar, uint32_t ph) {
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(smem_u32(bar), ph) && globaltimer_ns() - t0 < 100000000ull) {
+      }
+    };
+    for (int i = 0; i < kSlots; ++i)
+      if (ctl->tma_fill[i] >= 0) settle(&ctl->kv_full[i], (ctl->tma_fill[i] / kSlots) & 1);
+    for (int i = 0; i < 2; ++i)
+      if (ctl->tma_q[i] >= 0) settle(&ctl->q_full[i], (ctl->tma_q[i] >> 1) & 1);
+  }
   __syncthreads();
   if (warp == kMmaWarp) {
     __syncwarp();
@@ -698,11 +821,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs a) {
     r = h - hk * a.rep;
     if (part == 0) {
       const int i = (b - a.cu[g]) * a.rep + r;
-      const int row_tiles = ((a.cu[g + 1] - a.cu[g]) * a.rep + kTile - 1) / kTile;
-      idx = static_cast<long long>(hk) * row_tiles + i / kTile;
-      r = i % kTile;
+      const int row_tiles = ((a.cu[g + 1] - a.cu[g]) * a.rep + a.row_tile - 1) / a.row_tile;
+      idx = static_cast<long long>(hk) * row_tiles + i / a.row_tile;
+      r = i % a.row_tile;
     }
-    x0 = a.starts[e] + idx * n;
+    x0 = a.starts[e] + idx * (n + kItemCost) + kItemCost;
     x1 = x0 + n;
     return true;
   };
@@ -735,9 +858,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs a) {
   if (lane == 0 && a.lse) a.lse[row] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-template <class K>
-cudaError_t launch_after(K kern, int grid, int block, size_t smem, const AttnArgs& a,
-                         cudaStream_t st) {
+template <class K, class... Args>
+cudaError_t launch_after(K kern, int grid, int block, size_t smem, cudaStream_t st,
+                         const Args&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
@@ -748,20 +871,26 @@ cudaError_t launch_after(K kern, int grid, int block, size_t smem, const AttnArg
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+struct AttnMaps {
+  CUtensorMap k, v, q_group, q_own;
+};
+
 template <class E>
-cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
+cudaError_t launch(const AttnArgs& a, const AttnMaps& m, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(attn_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(kAttnSmem));
   if (e != cudaSuccess) return e;
   plan_kernel<<<1, kPlanThreads, 0, st>>>(a);
   e = cudaGetLastError();
-  if (e == cudaSuccess) e = launch_after(attn_kernel<E>, a.ctas, kAttnThreads, kAttnSmem, a, st);
+  if (e == cudaSuccess)
+    e = launch_after(attn_kernel<E>, a.ctas, kAttnThreads, kAttnSmem, st, a, m.k, m.v, m.q_group,
+                     m.q_own);
   const int per = kJoinThreads / 32;
   if (e == cudaSuccess)
-    e = launch_after(join_kernel<E>, (a.B * a.Hq + per - 1) / per, kJoinThreads, 0, a, st);
+    e = launch_after(join_kernel<E>, (a.B * a.Hq + per - 1) / per, kJoinThreads, 0, st, a);
   return e;
 }
 
@@ -834,6 +963,40 @@ extern "C" int rz_group_decode_attn(const void* q, const int64_t* q_stride, cons
   a.D = D;
   a.rep = Hq / Hkv;
   a.ctas = num_sms() < kMaxCtas ? num_sms() : kMaxCtas;
+  a.row_tile = kTile / a.rep * a.rep;
+  // Q as (D, heads, requests): boxes of 64 columns by a KV head's query heads
+  // by the requests of an item.  An axis of one element may come with any
+  // stride: it is given the least that a map takes.
+  AttnMaps m;
+  const auto bytes = [](int64_t stride, int64_t size) {
+    return static_cast<uint64_t>(size > 1 && stride > 0 ? stride * 2 : 16);
+  };
+  {
+    const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(Hq),
+                              static_cast<uint64_t>(B)};
+    const uint64_t st[2] = {bytes(q_stride[1], Hq), bytes(q_stride[0], B)};
+    uint32_t box[3] = {64, static_cast<uint32_t>(a.rep), static_cast<uint32_t>(kTile / a.rep)};
+    if ((Hq > 1 && q_stride[1] <= 0) || (B > 1 && q_stride[0] <= 0)) return RZ_ERR_UNSUPPORTED;
+    if (!make_tmap_16bit(&m.q_group, q, 3, dims, st, box)) return RZ_ERR_UNSUPPORTED;
+    box[2] = 1;
+    if (!make_tmap_16bit(&m.q_own, q, 3, dims, st, box)) return RZ_ERR_UNSUPPORTED;
+  }
+  m.k = m.v = m.q_own;
+  a.paged_tma = n_pages > 0 && page_size % 8 == 0 &&
+                (page_size % kTile == 0 || kTile % page_size == 0);
+  if (a.paged_tma) {
+    const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(Hkv),
+                              static_cast<uint64_t>(page_size), static_cast<uint64_t>(n_pages)};
+    const uint32_t box[4] = {64, 1, static_cast<uint32_t>(page_size < kTile ? page_size : kTile),
+                             1};
+    for (int i = 0; i < 2; ++i) {
+      const int64_t* ks = kv_stride + 3 * i;
+      const uint64_t st[3] = {bytes(ks[2], Hkv), bytes(ks[1], page_size), bytes(ks[0], n_pages)};
+      if ((Hkv > 1 && ks[2] <= 0) || (page_size > 1 && ks[1] <= 0) || (n_pages > 1 && ks[0] <= 0) ||
+          !make_tmap_16bit(i == 0 ? &m.k : &m.v, i == 0 ? k_cache : v_cache, 4, dims, st, box))
+        a.paged_tma = 0;  // a stride that no map takes: the copies do
+    }
+  }
   uint8_t* w8 = static_cast<uint8_t*>(ws);
   a.starts = reinterpret_cast<long long*>(w8 + L.starts);
   a.clen = reinterpret_cast<int32_t*>(w8 + L.clen);
@@ -845,6 +1008,6 @@ extern "C" int rz_group_decode_attn(const void* q, const int64_t* q_stride, cons
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(RZ_PROF_SMALL, 3, st);
   const cudaError_t e =
-      dtype == RZ_DTYPE_BF16 ? launch<__nv_bfloat16>(a, st) : launch<__half>(a, st);
+      dtype == RZ_DTYPE_BF16 ? launch<__nv_bfloat16>(a, m, st) : launch<__half>(a, m, st);
   return e == cudaSuccess ? RZ_OK : RZ_ERR_CUDA;
 }

@@ -83,6 +83,11 @@ bool device_ok();  // current device is sm_103 (or newer family member we compil
 bool make_tmap_bf16(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer,
                     uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
 
+// A map of 16-bit elements with `rank` <= 5 dimensions (innermost first; strides
+// in bytes of all but the innermost), 128-byte swizzle, zeros outside.
+bool make_tmap_16bit(CUtensorMap* tm, const void* base, int rank, const uint64_t* dims,
+                     const uint64_t* strides, const uint32_t* box);
+
 // ---- launch-class timing (rz_profile.cu): while rz_profile_begin() is in
 // effect, brackets the launches made in its lifetime with CUDA events on
 // `st` (classes RZ_PROF_*, `launches` kernels); otherwise does nothing.

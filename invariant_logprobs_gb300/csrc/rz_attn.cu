@@ -17,22 +17,26 @@
 // attn_kernel (one persistent CTA per SM), join_kernel (a warp per query row).
 //
 // attn_kernel, per tile: S = Q K^T (128 rows x 128 tokens, tcgen05, fp32 in
-// TMEM), the softmax terms P in 16 bits back into TMEM, O += P V with P as
-// the TMEM operand.
-//   warps 0-3  softmax: thread = query row = TMEM lane, so maximum, sum and
-//              the rescaling of O need no exchange between threads.  The
-//              reference m moves only when a row's maximum has grown by more
-//              than 8 (a factor 2^8, far inside fp32's and fp16's range), so
-//              O is rarely rescaled.  Warps without rows only keep step.
-//   warp 4     TMA: query rows, and K and V of full tiles page by page (page
+// TMEM), the softmax terms P in 16 bits over S's place in TMEM, O += P V with
+// P as the TMEM operand.
+//   warps 0-7  softmax, two groups of four: thread = query row = TMEM lane, so
+//              maximum, sum and the rescaling of O need no exchange between
+//              threads.  Group g takes every other tile, with an O, m and l of
+//              its own (a part's two halves are joined like any two parts):
+//              while one group waits for a product or writes an item out, the
+//              other works, also across items.  The reference m moves only
+//              when a row's maximum has grown by more than 8 (a factor 2^8,
+//              far inside fp32's and fp16's range), so O is rarely rescaled.
+//              Warps without rows only keep step.
+//   warp 8     TMA: query rows, and K and V of full tiles page by page (page
 //              sizes 8, 16, 32, 64 and multiples of 128), one lane a page.
-//   warps 5-8  16-byte asynchronous copies for every other tile, which zero
+//   warps 9-12 16-byte asynchronous copies for every other tile, which zero
 //              what is not there: 0 times a stray NaN of V would be NaN.
-//   warp 9     TMEM owner and MMA issuer: S of tile j+1 before P V of tile j.
+//   warp 13    TMEM owner and MMA issuer: S of tile j+1 before P V of tile j.
 // A tile's K and V are 64 KB at 128 columns; at its share of the memory an SM
 // takes 2,800 clocks for that, while the two products take 1,100 and the
-// softmax of a full warp about 1,000: the memory is what bounds it, whatever
-// the number of rows.
+// softmax of a full warp about 2,400 (every other tile): the memory is what
+// bounds it, whatever the number of rows.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -48,8 +52,9 @@ namespace {
 constexpr int kTile = 128;      // tokens per tile, query rows per item
 constexpr int kMaxD = 128;
 constexpr int kMaxCtas = 152;   // persistent CTAs at most (workspace size)
-constexpr int kSoftWarps = 4, kTmaWarp = 4, kCopyWarp0 = 5, kMmaWarp = 9;
-constexpr int kCopyWarps = kMmaWarp - kCopyWarp0;
+constexpr int kGroups = 2, kGroupWarps = 4;  // softmax groups
+constexpr int kTmaWarp = kGroups * kGroupWarps, kCopyWarp0 = kTmaWarp + 1, kCopyWarps = 4;
+constexpr int kMmaWarp = kCopyWarp0 + kCopyWarps;
 constexpr int kAttnThreads = 32 * (kMmaWarp + 1);
 constexpr int kSlots = 5;       // ring of K and V tiles
 constexpr uint32_t kHalf = kTile * 128;       // 128 rows x 64 columns, 16 KB
@@ -59,8 +64,9 @@ constexpr uint32_t kSmemQ = 0;                             // two buffers
 constexpr uint32_t kSmemKv = kSmemQ + 2 * kSlotBytes;
 constexpr uint32_t kSmemCtl = kSmemKv + kSlots * kSlotBytes;
 constexpr uint32_t kAttnSmem = kSmemCtl + 1024 + 1024;     // control block, alignment
-// TMEM columns: O, two S, two P
-constexpr uint32_t kColO = 0, kColS = 128, kColP = 384;
+constexpr int kLag = 3;         // copied fills issued but not yet announced
+// TMEM columns of a group: O, then S; P takes the first half of S's
+constexpr uint32_t kColO = 0, kColS = 128, kColGroup = 256;
 constexpr float kGrow = 8.f;
 // What beginning and ending an item costs, in tiles: the line that is cut
 // into runs has this many empty places before each item's tiles.
@@ -81,7 +87,7 @@ struct AttnArgs {
   long long* starts;  // [P + B + 1] first tile of each entry
   int32_t* clen;      // [P + B] clean lengths
   int32_t* cu;        // [P + 1] clean offsets
-  float *o_base, *o_extra;    // [2][B * Hq][D], [ctas][128][D]
+  float *o_base, *o_extra;    // [2][groups][B * Hq][D], [ctas][groups][128][D]
   float2 *ml_base, *ml_extra;
 };
 
@@ -96,10 +102,11 @@ AttnLayout attn_layout(int64_t B, int64_t P, int64_t Hq, int64_t D) {
   L.clen = L.starts + al256((e + 1) * 8);
   L.cu = L.clen + al256(e * 4);
   L.ml_base = L.cu + al256((static_cast<size_t>(P) + 1) * 4);
-  L.ml_extra = L.ml_base + al256(2 * rows * 8);
-  L.o_base = L.ml_extra + al256(static_cast<size_t>(kMaxCtas) * kTile * 8);
-  L.o_extra = L.o_base + al256(2 * rows * static_cast<size_t>(D) * 4);
-  L.total = L.o_extra + al256(static_cast<size_t>(kMaxCtas) * kTile * static_cast<size_t>(D) * 4);
+  L.ml_extra = L.ml_base + al256(2 * kGroups * rows * 8);
+  L.o_base = L.ml_extra + al256(static_cast<size_t>(kMaxCtas) * kGroups * kTile * 8);
+  L.o_extra = L.o_base + al256(2 * kGroups * rows * static_cast<size_t>(D) * 4);
+  L.total = L.o_extra +
+            al256(static_cast<size_t>(kMaxCtas) * kGroups * kTile * static_cast<size_t>(D) * 4);
   return L;
 }
 
@@ -165,7 +172,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs a) {
   };
   long long sum = 0;
   for (int e = e0; e < e1; ++e) {
-    const int len = entry_len(a, e, bad);
+    int len = entry_len(a, e, bad);
+    if (tiles(e, len) >= 1ll << 31) {  // more than 2^38 keys: no such cache
+      bad |= RZ_DEVERR_PAGES;
+      len = 0;
+    }
     a.clen[e] = len;
     sum += tiles(e, len);
   }
@@ -217,9 +228,9 @@ struct Walk {
     len = a.clen[e];
     n_tiles = (len + kTile - 1) / kTile;
     const int places = n_tiles + kItemCost;
-    const long long at = x - a.starts[e];
-    const long long item = at / places;
-    const int p0 = static_cast<int>(at - item * places);
+    const int at = static_cast<int>(x - a.starts[e]);
+    const int item = at / places;
+    const int p0 = at - item * places;
     const int p1 = end - x < places - p0 ? p0 + static_cast<int>(end - x) : places;
     taken = p1 - p0;
     t0 = max(p0 - kItemCost, 0);
@@ -228,16 +239,18 @@ struct Walk {
     if (e < a.P) {
       const int group_rows = (a.cu[e + 1] - a.cu[e]) * a.rep;
       const int row_tiles = (group_rows + a.row_tile - 1) / a.row_tile;
-      head = static_cast<int>(item / row_tiles);
-      row_tile = static_cast<int>(item) - head * row_tiles;
+      head = item / row_tiles;
+      row_tile = item - head * row_tiles;
       rows = min(a.row_tile, group_rows - row_tile * a.row_tile);
     } else {
-      head = static_cast<int>(item);
+      head = item;
       row_tile = 0;
       rows = a.rep;
     }
   }
   __device__ __forceinline__ void next() { x += taken; }
+  // the softmax group of tile t: alternating, and from item to item
+  __device__ __forceinline__ int group(int t) const { return (t + head + e) & 1; }
   // request and query head of row r of the part
   __device__ __forceinline__ void row(const AttnArgs& a, int r, int& b, int& h) const {
     if (e < a.P) {
@@ -252,8 +265,9 @@ struct Walk {
 };
 
 struct AttnCtl {
-  uint64_t kv_full[kSlots], kv_empty[kSlots], go[kCopyWarps];
-  uint64_t q_full[2], q_empty[2], s_full[2], s_empty[2], p_full[2], pv_done[2], o_free, drain;
+  uint64_t kv_full[kSlots], kv_empty[kSlots], go[kSlots];
+  uint64_t q_full[2], q_empty[2], s_full[kGroups], p_full[kGroups], pv_done[kGroups];
+  uint64_t o_free[kGroups], drain;
   uint32_t mask[kMaskRing][4];
   uint32_t tmem;
   int abort;
@@ -269,7 +283,7 @@ __device__ __forceinline__ void attn_abort(AttnCtl* c, int* err) {
 __device__ __forceinline__ bool warp_wait(AttnCtl* c, uint64_t* bar, uint32_t parity, int* err) {
   int ok = 1;
   if ((threadIdx.x & 31) == 0) {
-    ok = mbar_wait(bar, parity, const_cast<volatile int*>(&c->abort), kWaitLimitNs) ? 1 : 0;
+    ok = mbar_wait<true>(bar, parity, const_cast<volatile int*>(&c->abort), kWaitLimitNs) ? 1 : 0;
     if (!ok) attn_abort(c, err);
   }
   ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -302,16 +316,50 @@ __device__ __forceinline__ void load_rows_n(uint32_t dst, const uint8_t* row, ui
   }
 }
 
-// Whether a tile of the part comes by TMA: every token there and every page
-// of it in the pool (pg: this lane's page, of the tile's first `n`).
-__device__ __forceinline__ bool by_tma(const AttnArgs& a, const Walk& w, const int32_t* tab, int t,
-                                       int& pg, int& n) {
-  if (!a.paged_tma || (t + 1) * static_cast<long long>(kTile) > w.len) return false;
-  n = a.page < kTile ? kTile / a.page : 1;
-  const int first = static_cast<int>(static_cast<long long>(t) * kTile / a.page);
-  const int lane = threadIdx.x & 31;
-  pg = lane < n ? tab[first + lane] : 0;
-  return __all_sync(0xffffffffu, pg >= 0 && pg < a.n_pages);
+// Page ids of the tiles of a part, 32 pages (or, with pages of 128 and more,
+// 32 tiles) to a load, the next load under way while these are used: a load
+// for each tile would put its latency into every tile.
+struct PageIds {
+  const int32_t* tab;
+  int per_tile;   // pages of a tile; 1 where a page holds whole tiles
+  int per_load;   // tiles of a load
+  int t_at, end;  // tiles of `now` begin here; tiles of the part end here
+  int now, next;
+
+  __device__ __forceinline__ int fetch(const AttnArgs& a, int t) const {
+    const int lane = threadIdx.x & 31;
+    if (t + lane / per_tile >= end) return -1;
+    return tab[a.page < kTile ? t * per_tile + lane
+                              : static_cast<int>(static_cast<uint32_t>(t + lane) * kTile /
+                                                 static_cast<uint32_t>(a.page))];
+  }
+  __device__ __forceinline__ void init(const AttnArgs& a, const int32_t* row, int t0, int t1) {
+    tab = row;
+    per_tile = a.page < kTile ? kTile / a.page : 1;
+    per_load = 32 / per_tile;
+    t_at = t0;
+    end = t1;
+    now = fetch(a, t0);
+    next = fetch(a, t0 + per_load);
+  }
+  // This lane's page of full tile t (lanes below per_tile); t moves up by one.
+  // false: a page is not in the pool.
+  __device__ __forceinline__ bool get(const AttnArgs& a, int t, int& pg) {
+    if (t - t_at >= per_load) {
+      t_at += per_load;
+      now = next;
+      next = fetch(a, t_at + per_load);
+    }
+    const int lane = threadIdx.x & 31;
+    pg = __shfl_sync(0xffffffffu, now, ((t - t_at) * per_tile + lane) & 31);
+    return __all_sync(0xffffffffu, lane >= per_tile || (pg >= 0 && pg < a.n_pages));
+  }
+};
+
+// Whether a tile of the part may come by TMA: every token is there.  (A full
+// tile with a page outside the pool is the copy warps' as well.)
+__device__ __forceinline__ bool full_tile(const AttnArgs& a, const Walk& w, int t) {
+  return a.paged_tma && t < w.len / kTile;
 }
 
 __device__ __forceinline__ const int32_t* page_row(const AttnArgs& a, const Walk& w) {
@@ -330,66 +378,70 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   return pack_f16x2(lo, hi);
 }
 
-// What the softmax does to raw scores on the rare paths: turn the sign (a
-// negative scale), drop them (no scale), -inf at tokens that are not there.
+// The softmax takes a thread's 128 scores 32 columns at a time, in loops that
+// are not unrolled: with ten warps in seven pieces of code, straight-line
+// copies of these loops ran out of the instruction cache (twice as many cycles
+// waiting for instructions as issuing them).
+//
+// What it does to raw scores on the rare paths: turn the sign (a negative
+// scale), drop them (no scale), -inf at tokens that are not there.
 __device__ __forceinline__ void adjust(uint32_t (&s)[32], uint32_t bits, bool flip, bool zero) {
+  const uint32_t sign = flip ? 0x80000000u : 0u;
+  const uint32_t keep = zero ? 0u : 0xffffffffu;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    s[i] = zero ? 0u : (flip ? s[i] ^ 0x80000000u : s[i]);
-    if (!((bits >> i) & 1u)) s[i] = 0xff800000u;
-  }
+  for (int i = 0; i < 32; ++i)
+    s[i] = (bits >> i) & 1u ? (s[i] ^ sign) & keep : 0xff800000u;
 }
 
-// One half (64 columns) of a thread's scores, by how much of it is there.
-// The selects of a partly filled half would double the instructions of a full
-// one, so the three have code of their own (the choice is the warp's).
-enum HalfKind { kHalfFull, kHalfPart, kHalfNone };
-__device__ __forceinline__ HalfKind half_kind(uint32_t b0, uint32_t b1, bool general) {
-  if ((b0 | b1) == 0u) return kHalfNone;
-  return (b0 & b1) == 0xffffffffu && !general ? kHalfFull : kHalfPart;
-}
+struct SoftArgs {
+  uint32_t bits[4];  // the tile's tokens
+  bool general;      // flip or zero
+  bool flip, zero;
+  float sl;
+};
 
-template <bool kPart>
-__device__ __forceinline__ float half_max(uint32_t sc, uint32_t b0, uint32_t b1, bool flip,
-                                          bool zero) {
+// Maximum of a thread's scores times sl.
+__device__ __forceinline__ float tile_max(uint32_t sc, const SoftArgs& x) {
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-  uint32_t s[2][32];
-  tmem_ld32(sc, s[0]);
-  tmem_ld32(sc + 32, s[1]);
-  tmem_ld_wait();
-  if (kPart) {
-    adjust(s[0], b0, flip, zero);
-    adjust(s[1], b1, flip, zero);
-  }
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t bits = c == 0 ? x.bits[0] : c == 1 ? x.bits[1] : c == 2 ? x.bits[2] : x.bits[3];
+    if (bits == 0u) continue;
+    uint32_t s[32];
+    tmem_ld32(sc + 32 * c, s);
+    tmem_ld_wait();
+    if (bits != 0xffffffffu || x.general) adjust(s, bits, x.flip, x.zero);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    mx[i & 1] = fmaxf(mx[i & 1], __uint_as_float(s[0][i]));
-    mx[2 + (i & 1)] = fmaxf(mx[2 + (i & 1)], __uint_as_float(s[1][i]));
+    for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
   }
-  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * x.sl;
 }
 
-// The terms 2^(sl s - ref) into P, in 16 bits; returns their sum.
-template <class E, bool kPart>
-__device__ __forceinline__ float half_terms(uint32_t sc, uint32_t pc, uint32_t b0, uint32_t b1,
-                                            bool flip, bool zero, float sl, float ref) {
+// The terms 2^(sl s - ref) in 16 bits, over the scores' own columns (32 scores
+// at 32 c become 16 columns at 16 c, behind what is still to be read); their
+// sum.  `here` tokens belong to the tile; columns past them (to a multiple of
+// 16) are no part of the second product.
+template <class E>
+__device__ __forceinline__ float tile_terms(uint32_t sc, const SoftArgs& x, int here, float ref) {
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  uint32_t s[2][32], pk[32];
-  tmem_ld32(sc, s[0]);
-  tmem_ld32(sc + 32, s[1]);
-  tmem_ld_wait();
-  if (kPart) {
-    adjust(s[0], b0, flip, zero);
-    adjust(s[1], b1, flip, zero);
-  }
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    if (here <= 32 * c) break;
+    const uint32_t bits = c == 0 ? x.bits[0] : c == 1 ? x.bits[1] : c == 2 ? x.bits[2] : x.bits[3];
+    uint32_t s[32], pk[16];
+    tmem_ld32(sc + 32 * c, s);
+    tmem_ld_wait();
+    if (bits != 0xffffffffu || x.general) adjust(s, bits, x.flip, x.zero);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const float p0 = ex2_approx(fmaf(__uint_as_float(s[i >> 4][2 * (i & 15)]), sl, -ref));
-    const float p1 = ex2_approx(fmaf(__uint_as_float(s[i >> 4][2 * (i & 15) + 1]), sl, -ref));
-    acc[i & 3] += p0 + p1;
-    pk[i] = pack2<E>(p0, p1);
+    for (int i = 0; i < 16; ++i) {
+      const float s0 = __uint_as_float(s[2 * i]), s1 = __uint_as_float(s[2 * i + 1]);
+      const float p0 = ex2_approx(fmaf(s0, x.sl, -ref));
+      const float p1 = ex2_approx(fmaf(s1, x.sl, -ref));
+      acc[i & 3] += p0 + p1;
+      pk[i] = pack2<E>(p0, p1);
+    }
+    tmem_st16(sc + 16 * c, pk);
   }
-  tmem_st32(pc, pk);
   return (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
@@ -408,21 +460,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&ctl->kv_full[s], 1);
+      mbar_init(&ctl->kv_full[s], kCopyWarps);
       mbar_init(&ctl->kv_empty[s], 1);
+      mbar_init(&ctl->go[s], 1);
       ctl->tma_fill[s] = -1;
     }
-    for (int i = 0; i < kCopyWarps; ++i) mbar_init(&ctl->go[i], 1);
     ctl->tma_q[0] = ctl->tma_q[1] = -1;
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ctl->q_full[b], 1);
       mbar_init(&ctl->q_empty[b], 1);
-      mbar_init(&ctl->s_full[b], 1);
-      mbar_init(&ctl->s_empty[b], kSoftWarps);
-      mbar_init(&ctl->p_full[b], kSoftWarps);
-      mbar_init(&ctl->pv_done[b], 1);
     }
-    mbar_init(&ctl->o_free, kSoftWarps);
+    for (int g = 0; g < kGroups; ++g) {
+      mbar_init(&ctl->s_full[g], 1);
+      mbar_init(&ctl->p_full[g], kGroupWarps);
+      mbar_init(&ctl->pv_done[g], 1);
+      mbar_init(&ctl->o_free[g], kGroupWarps);
+    }
     mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -449,17 +502,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   w.init(a, blockIdx.x);
 
   // Fill f of the ring is K of tile f / 2, then its V.  The TMA warp claims
-  // every slot in order; a fill that is not its own it hands to copy warp
-  // f mod 4 (at most two such ahead of what that warp has done, as the ring
-  // is shorter than eight).
+  // every slot in order; a fill that is not its own it hands to the copy
+  // warps through the slot's `go`.
   const uint32_t halves = a.D > 64 ? 2u : 1u;
   if (warp == kTmaWarp) {
     // ---------------------------------------------------------------- TMA
     uint32_t tile = 0;
     int item = 0;
     bool ok = true;
+    PageIds ids;
     while (ok && w.part(a)) {
-      const int32_t* tab = page_row(a, w);
+      if (a.paged_tma) ids.init(a, page_row(a, w), w.t0, min(w.t1, w.len / kTile));
       // the part's query rows: whole requests' heads of this KV head
       const int qb = item & 1;
       if (item >= 2 && !(ok = warp_wait(ctl, &ctl->q_empty[qb], (item / 2 + 1) & 1u, a.err))) break;
@@ -475,16 +528,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       ++item;
       for (int t = w.t0; ok && t < w.t1; ++t, ++tile) {
-        int pg = 0, n = 0;
-        const bool mine = by_tma(a, w, tab, t, pg, n);
-        const int row = static_cast<int>(static_cast<long long>(t) * kTile % a.page);
+        int pg = 0;
+        const bool mine = full_tile(a, w, t) && ids.get(a, t, pg);
+        const int row = a.page < kTile
+                            ? 0
+                            : static_cast<int>(static_cast<uint32_t>(t) * kTile %
+                                               static_cast<uint32_t>(a.page));
         for (uint32_t kv = 0; kv < 2; ++kv) {
           const uint32_t f = 2 * tile + kv, slot = f % kSlots;
           if (f >= kSlots &&
               !(ok = warp_wait(ctl, &ctl->kv_empty[slot], (f / kSlots + 1) & 1u, a.err)))
             break;
           if (!mine) {
-            if (lane == 0) mbar_arrive(&ctl->go[f % kCopyWarps]);
+            if (lane == 0) mbar_arrive(&ctl->go[slot]);
             continue;
           }
           if (kv == 0 && lane < 4) ctl->mask[tile % kMaskRing][lane] = 0xffffffffu;
@@ -492,10 +548,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (lane == 0) {
             ctl->tma_fill[slot] = static_cast<int>(f);
             mbar_arrive_expect_tx(&ctl->kv_full[slot], halves * kHalf);
+            for (int i = 1; i < kCopyWarps; ++i) mbar_arrive(&ctl->kv_full[slot]);
           }
           __syncwarp();
           uint8_t* dst = smem + kSmemKv + slot * kSlotBytes;
-          if (lane < n)
+          if (lane < ids.per_tile)
             for (uint32_t i = 0; i < halves; ++i)
               tma_load_4d(dst + i * kHalf + lane * a.page * 128, kv == 0 ? &tm_k : &tm_v,
                           &ctl->kv_full[slot], 64 * i, w.head, row, pg);
@@ -507,147 +564,190 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // ---------------------------------------------------------------- copies
     // Tiles with fewer than 128 tokens or a page outside the pool, and all
     // tiles where the page size does not fit: 16-byte copies that zero what
-    // is not there.
-    const uint32_t cw = warp - kCopyWarp0;
-    const bool is_k = (cw & 1u) == 0;
+    // is not there, 32 rows a warp.
+    const int cw = warp - kCopyWarp0;
     const int chunks = a.D / 8;
-    uint32_t tile = 0, done = 0;
+    uint32_t tile = 0, phases = 0;      // parity of each slot's `go`
+    uint32_t queue = 0;                 // slots issued and not announced, 4 bits each
+    int queued = 0;
     bool ok = true;
     int bad = 0;
+    PageIds ids;
+    const auto announce = [&](int left) {  // all but `left`; their copies are done
+      fence_proxy_async_smem();
+      __syncwarp();
+      for (; queued > left; --queued) {
+        if (lane == 0) mbar_arrive(&ctl->kv_full[(queue >> (4 * (queued - 1))) & 15u]);
+      }
+    };
     while (ok && w.part(a)) {
       const int32_t* tab = page_row(a, w);
+      if (a.paged_tma) ids.init(a, tab, w.t0, min(w.t1, w.len / kTile));
       for (int t = w.t0; ok && t < w.t1; ++t, ++tile) {
-        if ((tile & 1u) != (cw >> 1)) continue;
-        int unused_pg, unused_n;
-        if (by_tma(a, w, tab, t, unused_pg, unused_n)) continue;
-        const uint32_t slot = (2 * tile + (cw & 1u)) % kSlots;
-        if (!(ok = warp_wait(ctl, &ctl->go[cw], done & 1u, a.err))) break;
-        ++done;
-        const uint8_t* src = static_cast<const uint8_t*>(is_k ? a.k : a.v);
-        const long long* st = is_k ? a.ks : a.vs;
-        const uint32_t dst = base + kSmemKv + slot * kSlotBytes;
+        if (full_tile(a, w, t)) {
+          int pg;
+          if (ids.get(a, t, pg)) continue;
+        }
         // K: the tokens there are (the other scores are never looked at).  V:
         // up to the product's depth, zeros where there is no token, as 0
         // times a stray NaN would be NaN.
         const uint32_t here = static_cast<uint32_t>(min(w.len - t * kTile, kTile));
-        const uint32_t deep = is_k ? here : (here + 15) / 16 * 16;
-        int pg[4];
-        uint32_t off[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {  // the page ids' loads overlap
-          const uint32_t i = 32 * g + lane;
-          pg[g] = -1;
-          off[g] = 0;
-          if (i < here) {
-            const uint32_t tok = static_cast<uint32_t>(t) * kTile + i;
-            const uint32_t j = tok / static_cast<uint32_t>(a.page);
-            off[g] = tok - j * static_cast<uint32_t>(a.page);
-            pg[g] = tab[j];
-            if (pg[g] < 0 || pg[g] >= a.n_pages) {
-              pg[g] = -1;
-              bad = RZ_DEVERR_PAGES;
-            }
+        const uint32_t i = 32 * cw + lane;
+        int pg = -1;
+        uint32_t off = 0;
+        if (i < here) {
+          const uint32_t tok = static_cast<uint32_t>(t) * kTile + i;
+          const uint32_t j = tok / static_cast<uint32_t>(a.page);
+          off = tok - j * static_cast<uint32_t>(a.page);
+          pg = tab[j];
+          if (pg < 0 || pg >= a.n_pages) {
+            pg = -1;
+            bad = RZ_DEVERR_PAGES;
           }
         }
+        const uint32_t read = __ballot_sync(0xffffffffu, pg >= 0);
+        const uint32_t fill_k = __ballot_sync(0xffffffffu, i < here);
+        const uint32_t fill_v = __ballot_sync(0xffffffffu, i < (here + 15) / 16 * 16);
 #pragma unroll 1
-        for (int g = 0; g < 4; ++g) {
-          const int page = g == 0 ? pg[0] : g == 1 ? pg[1] : g == 2 ? pg[2] : pg[3];
-          const uint32_t o = g == 0 ? off[0] : g == 1 ? off[1] : g == 2 ? off[2] : off[3];
-          const uint32_t read = __ballot_sync(0xffffffffu, page >= 0);
-          if (is_k && lane == 0) ctl->mask[tile % kMaskRing][g] = read;
-          const uint32_t fill = __ballot_sync(0xffffffffu, 32u * g + lane < deep);
-          if (fill == 0) continue;
-          const uint8_t* row = src;
-          if (page >= 0)
-            row += 2 * (page * st[0] + static_cast<long long>(o) * st[1] + w.head * st[2]);
-          if (chunks > 8) load_rows_n<16>(dst, row, read, fill, g, chunks);
-          else load_rows_n<8>(dst, row, read, fill, g, chunks);
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t slot = (2 * tile + kv) % kSlots;
+          uint64_t* bar = &ctl->go[slot];
+          const uint32_t ph = (phases >> slot) & 1u;
+          if (!__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), ph))) {
+            // nothing to do: what has been issued may be waited for by others
+            cp_async_wait<0>();
+            announce(0);
+            if (!(ok = warp_wait(ctl, bar, ph, a.err))) break;
+          }
+          phases ^= 1u << slot;
+          if (kv == 0 && lane == 0) ctl->mask[tile % kMaskRing][cw] = read;
+          const uint8_t* row = static_cast<const uint8_t*>(kv == 0 ? a.k : a.v);
+          const long long* st = kv == 0 ? a.ks : a.vs;
+          if (pg >= 0)
+            row += 2 * (pg * st[0] + static_cast<long long>(off) * st[1] + w.head * st[2]);
+          const uint32_t dst = base + kSmemKv + slot * kSlotBytes;
+          const uint32_t fill = kv == 0 ? fill_k : fill_v;
+          if (fill != 0) {
+            if (chunks > 8) load_rows_n<16>(dst, row, read, fill, cw, chunks);
+            else load_rows_n<8>(dst, row, read, fill, cw, chunks);
+          }
+          cp_async_commit();
+          queue = queue << 4 | slot;
+          if (++queued > kLag) {
+            cp_async_wait<kLag>();
+            announce(kLag);
+          }
         }
-        cp_async_commit();
-        cp_async_wait<0>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->kv_full[slot]);
       }
       w.next();
     }
+    cp_async_wait<0>();
+    announce(0);
     if (bad && a.err) atomicOr(a.err, bad);
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- products
     if (lane == 0) {
-      const uint32_t fmt = sizeof(E) == 2 && std::is_same<E, __nv_bfloat16>::value
-                               ? (1u << 7) | (1u << 10) : 0u;
+      const uint32_t fmt =
+          std::is_same<E, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u;
       const uint32_t depth = (a.D + 15) / 16;
       const uint32_t idesc_s = (1u << 4) | fmt | ((kTile >> 4) << 24);  // and N / 8 << 17
       const uint32_t idesc_o = (1u << 4) | fmt | (1u << 16) | ((2 * depth) << 17) |
                                ((kTile >> 4) << 24);
       const volatile int* abort = const_cast<volatile int*>(&ctl->abort);
       bool ok = true;
-      uint32_t tile = 0;   // S issued
-      int item = 0, o_items = 0;
+      uint32_t tile = 0;                      // S issued
+      uint32_t p_used = 0, o_used[kGroups] = {0, 0};  // p_full phases; parts begun
+      int item = 0;
       bool pend = false, pend_first = false;  // the tile whose P V is due
-      int pend_k = 0;                         // its tokens / 16
-      const auto pv = [&](uint32_t j, bool fresh, int steps) {
-        const uint32_t b = j & 1u, use = (j >> 1) & 1u;
-        const uint32_t f = 2 * j + 1;
-        const uint32_t slot = f % kSlots;
+      int pend_k = 0, pend_g = 0;             // its tokens / 16, its group
+      const auto pv = [&]() {
+        const uint32_t f = 2 * tile - 1, slot = f % kSlots;  // V of tile - 1
+        const int g = pend_g;
         if (!mbar_wait(&ctl->kv_full[slot], (f / kSlots) & 1u, abort, kWaitLimitNs) ||
-            !mbar_wait(&ctl->p_full[b], use, abort, kWaitLimitNs))
+            !mbar_wait(&ctl->p_full[g], (p_used >> g) & 1u, abort, kWaitLimitNs))
           return false;
-        if (fresh) {
-          if (o_items > 0 && !mbar_wait(&ctl->o_free, (o_items - 1) & 1u, abort, kWaitLimitNs))
+        p_used ^= 1u << g;
+        if (pend_first) {
+          const uint32_t used = g == 0 ? o_used[0]++ : o_used[1]++;
+          if (used > 0 && !mbar_wait(&ctl->o_free[g], (used - 1) & 1u, abort, kWaitLimitNs))
             return false;
-          ++o_items;
         }
         tc_fence_after();
-        const uint32_t v = base + kSmemKv + slot * kSlotBytes;
-        for (int k = 0; k < steps; ++k)
-          umma_f16_ts(tmem + kColO, tmem + kColP + 64 * b + 8 * k,
-                      sdesc_sw128(v + 2048u * k, kHalf, 1024u), idesc_o,
-                      (fresh && k == 0) ? 0u : 1u);
+        const uint64_t v = sdesc_sw128(base + kSmemKv + slot * kSlotBytes, kHalf, 1024u);
+        const uint32_t o = tmem + g * kColGroup + kColO, p = tmem + g * kColGroup + kColS;
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          if (k < pend_k)
+            umma_f16_ts(o, p + 8 * k, v + (2048u * k >> 4), idesc_o,
+                        (pend_first && k == 0) ? 0u : 1u);
         umma_commit(&ctl->kv_empty[slot]);
-        umma_commit(&ctl->pv_done[b]);
+        umma_commit(&ctl->pv_done[g]);
         return true;
       };
-      while (ok && w.part(a)) {
-        const uint32_t q = base + kSmemQ + (item & 1) * kSlotBytes;
-        if (!mbar_wait(&ctl->q_full[item & 1], (item >> 1) & 1u, abort, kWaitLimitNs)) {
-          ok = false;
-          break;
-        }
-        for (int t = w.t0; t < w.t1; ++t, ++tile) {
-          const uint32_t b = tile & 1u, use = (tile >> 1) & 1u;
-          const uint32_t f = 2 * tile;
-          const uint32_t slot = f % kSlots;
-          if (!mbar_wait(&ctl->kv_full[slot], (f / kSlots) & 1u, abort, kWaitLimitNs) ||
-              !mbar_wait(&ctl->s_empty[b], use ^ 1u, abort, kWaitLimitNs)) {
+      while (true) {
+        const bool more = ok && w.part(a);
+        if (!more && !(ok && pend)) break;
+        const int t_end = more ? w.t1 : 1;
+        uint64_t q = 0;
+        if (more) {
+          q = sdesc_sw128(base + kSmemQ + (item & 1) * kSlotBytes, 16u, 1024u);
+          if (!mbar_wait(&ctl->q_full[item & 1], (item >> 1) & 1u, abort, kWaitLimitNs)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const int n16 = (min(w.len - t * kTile, kTile) + 15) / 16;  // tokens / 16
-          const uint32_t idesc = idesc_s | (static_cast<uint32_t>(2 * n16) << 17);
-          const uint32_t k0 = base + kSmemKv + slot * kSlotBytes;
-          for (uint32_t k = 0; k < depth; ++k) {
-            const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32u;
-            umma_bf16(tmem + kColS + 128 * b, sdesc_sw128(q + off, 16u, 1024u),
-                      sdesc_sw128(k0 + off, 16u, 1024u), idesc, k > 0 ? 1u : 0u);
-          }
-          umma_commit(&ctl->kv_empty[slot]);
-          umma_commit(&ctl->s_full[b]);
-          if (t == w.t1 - 1) umma_commit(&ctl->q_empty[item & 1]);
-          if (pend && !pv(tile - 1, pend_first, pend_k)) {
-            ok = false;
-            break;
-          }
-          pend = true;
-          pend_first = t == w.t0;
-          pend_k = n16;
         }
-        ++item;
-        w.next();
+        // (after the last part: one more turn, for the last tile's P V)
+        for (int t = more ? w.t0 : 0; t < t_end; ++t) {
+          if (more) {
+            const uint32_t f = 2 * tile, slot = f % kSlots;
+            if (!mbar_wait(&ctl->kv_full[slot], (f / kSlots) & 1u, abort, kWaitLimitNs)) {
+              ok = false;
+              break;
+            }
+            // S[g] is free: P V of the group's tile before, issued earlier in
+            // this order, is what reads it last
+            tc_fence_after();
+            const int g = w.group(t);
+            const int n16 = (min(w.len - t * kTile, kTile) + 15) / 16;  // tokens / 16
+            const uint32_t idesc = idesc_s | (static_cast<uint32_t>(2 * n16) << 17);
+            const uint64_t k0 = sdesc_sw128(base + kSmemKv + slot * kSlotBytes, 16u, 1024u);
+            const uint32_t sc = tmem + g * kColGroup + kColS;
+            // the group's tile before may be the one whose P V is due (two
+            // parts of one tile each): then it goes first
+            if (pend && pend_g == g) {
+              if (!pv()) {
+                ok = false;
+                break;
+              }
+              pend = false;
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < kMaxD / 16; ++k) {
+              const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32u) >> 4;
+              if (k < depth) umma_bf16(sc, q + off, k0 + off, idesc, k > 0 ? 1u : 0u);
+            }
+            umma_commit(&ctl->kv_empty[slot]);
+            umma_commit(&ctl->s_full[g]);
+            if (t == w.t1 - 1) umma_commit(&ctl->q_empty[item & 1]);
+            if (pend && !pv()) {
+              ok = false;
+              break;
+            }
+            pend = true;
+            pend_first = t < w.t0 + 2;  // the group's first tile of the part
+            pend_k = n16;
+            pend_g = g;
+            ++tile;
+          } else {
+            ok = pv();
+            pend = false;
+          }
+        }
+        if (more) {
+          ++item;
+          w.next();
+        }
       }
-      if (ok && pend) ok = pv(tile - 1, pend_first, pend_k);
       if (!ok) attn_abort(ctl, a.err);
       // no MMA is in flight when TMEM is freed
       umma_commit(&ctl->drain);
@@ -655,107 +755,98 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const int r = warp * 32 + lane;
-    const bool flip = a.scale < 0.f, zero = a.scale == 0.f;
-    const float sl = zero ? 1.f : fabsf(a.scale);
-    uint32_t tile = 0;
+    const int g = warp / kGroupWarps, quad = warp % kGroupWarps;
+    const uint32_t lanes = tmem + g * kColGroup + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t sc = lanes + kColS;
+    const int r = quad * 32 + lane;
+    SoftArgs soft;
+    soft.flip = a.scale < 0.f;
+    soft.zero = a.scale == 0.f;
+    soft.general = soft.flip || soft.zero;
+    soft.sl = soft.zero ? 1.f : fabsf(a.scale);
+    uint32_t tile0 = 0;             // tiles of the parts before
+    uint32_t s_used = 0, pv_used = 0;  // phases
     bool ok = true;
     while (ok && w.part(a)) {
-      const bool live = warp * 32 < w.rows;
+      const bool live = quad * 32 < w.rows;
+      const int first = w.t0 + (w.group(w.t0) != g);  // this group's tiles: first, first + 2, ...
       float m = -INFINITY, l = 0.f;
-      for (int t = w.t0; t < w.t1; ++t, ++tile) {
-        const uint32_t b = tile & 1u, use = (tile >> 1) & 1u;
-        if (!(ok = warp_wait(ctl, &ctl->s_full[b], use, a.err))) break;
+      for (int t = first; t < w.t1; t += 2) {
+        if (!(ok = warp_wait(ctl, &ctl->s_full[g], s_used & 1u, a.err))) break;
+        ++s_used;
         tc_fence_after();
-        uint32_t bits[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) bits[i] = ctl->mask[tile % kMaskRing][i];
         if (live) {
-          const uint32_t sc = lanes + kColS + 128 * b;
-          const bool general = flip || zero;
-          const HalfKind h0 = half_kind(bits[0], bits[1], general);
-          const HalfKind h1 = half_kind(bits[2], bits[3], general);
-          float top = -INFINITY;
-          if (h0 == kHalfFull) top = half_max<false>(sc, 0u, 0u, false, false);
-          else if (h0 == kHalfPart) top = half_max<true>(sc, bits[0], bits[1], flip, zero);
-          if (h1 == kHalfFull) top = fmaxf(top, half_max<false>(sc + 64, 0u, 0u, false, false));
-          else if (h1 == kHalfPart)
-            top = fmaxf(top, half_max<true>(sc + 64, bits[2], bits[3], flip, zero));
-          top *= sl;
-          const bool grow = top > m + kGrow || (m == -INFINITY && top > m);
-          if (t > w.t0 && __any_sync(0xffffffffu, grow)) {
-            // O of the tiles before moves to the new reference
-            const uint32_t pj = tile - 1;
-            if (!(ok = warp_wait(ctl, &ctl->pv_done[pj & 1u], (pj >> 1) & 1u, a.err))) break;
-            tc_fence_after();
-            const float f = grow ? (m == -INFINITY ? 0.f : ex2_approx(m - top)) : 1.f;
-            for (int i = 0; i < a.D; i += 32) {
-              uint32_t o[32];
-              tmem_ld32(lanes + kColO + i, o);
-              tmem_ld_wait();
+          const uint32_t tile = tile0 + (t - w.t0);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st32(lanes + kColO + i, o);
+          for (int i = 0; i < 4; ++i) soft.bits[i] = ctl->mask[tile % kMaskRing][i];
+          const int here = min(w.len - t * kTile, kTile);
+          const float top = tile_max(sc, soft);
+          const bool grow = top > m + kGrow || (m == -INFINITY && top > m);
+          if (t > first) {
+            // the group's P V before this one: O may be touched
+            if (!(ok = warp_wait(ctl, &ctl->pv_done[g], pv_used & 1u, a.err))) break;
+            ++pv_used;
+            if (__any_sync(0xffffffffu, grow && r < w.rows)) {
+              // O of the tiles before moves to the new reference
+              tc_fence_after();
+              const float f = grow ? (m == -INFINITY ? 0.f : ex2_approx(m - top)) : 1.f;
+#pragma unroll 1
+              for (int i = 0; i < a.D; i += 32) {
+                uint32_t o[32];
+                tmem_ld32(lanes + kColO + i, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                tmem_st32(lanes + kColO + i, o);
+              }
+              l *= f;
+              if (grow) m = top;
             }
-            tmem_st_wait();
-            l *= f;
+          } else if (grow) {
+            m = top;
           }
-          if (grow) m = top;
-          const float ref = m == -INFINITY ? 0.f : m;
-          const uint32_t pc = lanes + kColP + 64 * b;
-          // a half without a token is no part of the second product, unless
-          // a page inside the length is missing: then its terms are zeros
-          const uint32_t here = static_cast<uint32_t>(w.len - t * kTile);
-          const auto terms = [&](HalfKind kind, uint32_t off, uint32_t b0, uint32_t b1) {
-            if (kind == kHalfFull)
-              l += half_terms<E, false>(sc + off, pc + off / 2, 0u, 0u, false, false, sl, ref);
-            else if (kind == kHalfPart || here > off)
-              l += half_terms<E, true>(sc + off, pc + off / 2, b0, b1, flip, zero, sl, ref);
-          };
-          terms(h0, 0, bits[0], bits[1]);
-          terms(h1, 64, bits[2], bits[3]);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->s_empty[b]);
+          l += tile_terms<E>(sc, soft, here, m == -INFINITY ? 0.f : m);
           tmem_st_wait();
-        } else {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->s_empty[b]);
+        } else if (t > first) {
+          if (!(ok = warp_wait(ctl, &ctl->pv_done[g], pv_used & 1u, a.err))) break;
+          ++pv_used;
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->p_full[b]);
+        if (lane == 0) mbar_arrive(&ctl->p_full[g]);
       }
       if (!ok) break;
-      // the part's result
-      const uint32_t pj = tile - 1;
-      if (!(ok = warp_wait(ctl, &ctl->pv_done[pj & 1u], (pj >> 1) & 1u, a.err))) break;
-      tc_fence_after();
-      if (live) {
-        long long at = static_cast<long long>(blockIdx.x) * kTile + r;
-        if (w.first && r < w.rows) {
-          int q, h;
-          w.row(a, r, q, h);
-          at = (static_cast<long long>(w.e < a.P ? 0 : a.B) + q) * a.Hq + h;
-        }
-        float* dst = (w.first ? a.o_base : a.o_extra) + at * a.D;
-        for (int i = 0; i < a.D; i += 32) {
-          uint32_t o[32];
-          tmem_ld32(lanes + kColO + i, o);
-          tmem_ld_wait();
-          if (r < w.rows) {
-#pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              if (i + k < a.D) st_global_v4(dst + i + k, o[k], o[k + 1], o[k + 2], o[k + 3]);
+      tile0 += w.t1 - w.t0;
+      if (first < w.t1) {
+        // this group's share of the part's result
+        if (!(ok = warp_wait(ctl, &ctl->pv_done[g], pv_used & 1u, a.err))) break;
+        ++pv_used;
+        tc_fence_after();
+        if (live) {
+          long long at = (static_cast<long long>(blockIdx.x) * kGroups + g) * kTile + r;
+          if (w.first && r < w.rows) {
+            int q, h;
+            w.row(a, r, q, h);
+            at = (static_cast<long long>((w.e < a.P ? 0 : kGroups) + g) * a.B + q) * a.Hq + h;
           }
+          float* dst = (w.first ? a.o_base : a.o_extra) + at * a.D;
+#pragma unroll 1
+          for (int i = 0; i < a.D; i += 32) {
+            uint32_t o[32];
+            tmem_ld32(lanes + kColO + i, o);
+            tmem_ld_wait();
+            if (r < w.rows) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 4)
+                if (i + k < a.D) st_global_v4(dst + i + k, o[k], o[k + 1], o[k + 2], o[k + 3]);
+            }
+          }
+          if (r < w.rows) (w.first ? a.ml_base : a.ml_extra)[at] = make_float2(m, l);
         }
-        if (r < w.rows) (w.first ? a.ml_base : a.ml_extra)[at] = make_float2(m, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->o_free[g]);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->o_free);
       w.next();
     }
   }
@@ -811,51 +902,54 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs a) {
     }
     g = lo;
   }
-  // the item's tiles [x0, x1) and the row in it, for prompt and own tokens
-  const auto item = [&](int part, long long& x0, long long& x1, int& r) {
+  float M = -INFINITY, L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int part = 0; part < 2; ++part) {
     const int e = part == 0 ? g : a.P + b;
-    if (e < 0) return false;
+    if (e < 0) continue;
     const int n = (a.clen[e] + kTile - 1) / kTile;
-    if (n == 0) return false;
+    if (n == 0) continue;
+    // the row's place in its item, and the item's tiles x0 .. x0 + n - 1
     long long idx = hk;
-    r = h - hk * a.rep;
+    int r = h - hk * a.rep;
     if (part == 0) {
       const int i = (b - a.cu[g]) * a.rep + r;
       const int row_tiles = ((a.cu[g + 1] - a.cu[g]) * a.rep + a.row_tile - 1) / a.row_tile;
       idx = static_cast<long long>(hk) * row_tiles + i / a.row_tile;
       r = i % a.row_tile;
     }
-    x0 = a.starts[e] + idx * (n + kItemCost) + kItemCost;
-    x1 = x0 + n;
-    return true;
-  };
-  float M = -INFINITY, L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int part = 0; part < 2; ++part) {
-    long long x0, x1;
-    int r;
-    if (!item(part, x0, x1, r)) continue;
+    const long long x0 = a.starts[e] + idx * (n + kItemCost) + kItemCost, x1 = x0 + n;
     const long long c0 = x0 / per, c1 = (x1 - 1) / per;
     for (long long c = c0; c <= c1; ++c) {
-      const long long at = c == c0 ? (static_cast<long long>(part == 0 ? 0 : a.B) + b) * a.Hq + h
-                                   : c * kTile + r;
-      const float2 ml = (c == c0 ? a.ml_base : a.ml_extra)[at];
-      const float* src = (c == c0 ? a.o_base : a.o_extra) + at * a.D;
-      const float mn = fmaxf(M, ml.x);
-      if (mn == -INFINITY) continue;  // no token yet
-      const float f = exp2f(M - mn), fe = exp2f(ml.x - mn);
-      L = L * f + ml.y * fe;
+      const long long t0 = (c == c0 ? x0 : c * per) - x0;
+      const long long t1 = (c == c1 ? x1 : (c + 1) * per) - x0;
+      for (int gr = 0; gr < kGroups; ++gr) {
+        // (t + head + e) & 1 is the group of tile t
+        if (t1 - t0 < 2 && ((t0 + hk + e) & 1) != gr) continue;
+        const long long at =
+            c == c0 ? (static_cast<long long>((part == 0 ? 0 : kGroups) + gr) * a.B + b) * a.Hq + h
+                    : (c * kGroups + gr) * kTile + r;
+        const float2 ml = (c == c0 ? a.ml_base : a.ml_extra)[at];
+        const float* src = (c == c0 ? a.o_base : a.o_extra) + at * a.D;
+        const float mn = fmaxf(M, ml.x);
+        if (mn == -INFINITY && !(ml.y != ml.y)) continue;  // no token yet
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        const float f = exp2f(M - ref), fe = exp2f(ml.x - ref);
+        L = L * f + ml.y * fe;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < a.D) o[i] = o[i] * f + src[lane + 32 * i] * fe;
-      M = mn;
+        for (int i = 0; i < 4; ++i)
+          if (lane + 32 * i < a.D) o[i] = o[i] * f + src[lane + 32 * i] * fe;
+        M = mn;
+      }
     }
   }
   E* out = static_cast<E*>(a.out) + row * a.D;
-  const float inv = M == -INFINITY ? 0.f : 1.f / L;
+  const bool none = M == -INFINITY && L == 0.f;  // no token
+  const float inv = none ? 0.f : 1.f / L;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (lane + 32 * i < a.D) put16(out + lane + 32 * i, o[i] * inv);
-  if (lane == 0 && a.lse) a.lse[row] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * kLn2;
+  if (lane == 0 && a.lse)
+    a.lse[row] = none ? -INFINITY : ((M == -INFINITY ? 0.f : M) + log2f(L)) * kLn2;
 }
 
 template <class K, class... Args>

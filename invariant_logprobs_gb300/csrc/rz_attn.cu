@@ -28,10 +28,11 @@
 //              when a row's maximum has grown by more than 8 (a factor 2^8,
 //              far inside fp32's and fp16's range), so O is rarely rescaled.
 //              Warps without rows only keep step.
-//   warp 8     TMA: query rows, and K and V of full tiles page by page (page
-//              sizes 8, 16, 32, 64 and multiples of 128), one lane a page.
-//   warps 9-12 16-byte asynchronous copies for every other tile, which zero
-//              what is not there: 0 times a stray NaN of V would be NaN.
+//   warp 8     TMA: query rows, and K and V page by page (page sizes 8, 16, 32,
+//              64 and multiples of 128), one lane a page.
+//   warps 9-12 16-byte asynchronous copies for other page sizes, and zeros in
+//              V past a partly filled tile's last token: 0 times a stray NaN
+//              would be NaN.
 //   warp 13    TMEM owner and MMA issuer: S of tile j+1 before P V of tile j.
 // A tile's K and V are 64 KB at 128 columns; at its share of the memory an SM
 // takes 2,800 clocks for that, while the two products take 1,100 and the
@@ -271,7 +272,11 @@ struct AttnCtl {
   uint32_t mask[kMaskRing][4];
   uint32_t tmem;
   int abort;
-  int tma_fill[kSlots], tma_q[2];  // last fill, item that a TMA copy was issued for; -1
+  // what a TMA copy was last issued for: a slot's barrier and its phase, a
+  // query buffer's item (null, -1: none)
+  uint64_t* tma_bar[kSlots];
+  uint32_t tma_phase[kSlots];
+  int tma_q[2];
 };
 static_assert(sizeof(AttnCtl) <= 1024, "control block");
 
@@ -310,9 +315,16 @@ __device__ __forceinline__ void load_rows_n(uint32_t dst, const uint8_t* row, ui
     const int r = sub + kStep * i;
     const uint8_t* p = reinterpret_cast<const uint8_t*>(
         __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r));
-    if (mine && (fill >> r) & 1u)
-      cp_async16(base + kStep * i * 128 + (((c & 7) ^ (r & 7)) << 4), p + 16 * c,
-                 (read >> r) & 1u ? 16u : 0u);
+    if (mine && ((read >> r) & 1u))
+      cp_async16(base + kStep * i * 128 + (((c & 7) ^ (r & 7)) << 4), p + 16 * c);
+  }
+  if (fill & ~read) {
+#pragma unroll 1
+    for (int i = 0; i < kLanes; ++i) {
+      const int r = sub + kStep * i;
+      if (mine && ((fill & ~read) >> r) & 1u)
+        st_shared_zero16(base + kStep * i * 128 + (((c & 7) ^ (r & 7)) << 4));
+    }
   }
 }
 
@@ -321,46 +333,41 @@ __device__ __forceinline__ void load_rows_n(uint32_t dst, const uint8_t* row, ui
 // for each tile would put its latency into every tile.
 struct PageIds {
   const int32_t* tab;
-  int per_tile;   // pages of a tile; 1 where a page holds whole tiles
-  int per_load;   // tiles of a load
-  int t_at, end;  // tiles of `now` begin here; tiles of the part end here
+  int per_tile;     // pages of a tile; 1 where a page holds whole tiles
+  int per_load;     // tiles of a load
+  int t_at, limit;  // tiles of `now` begin here; pages that hold tokens
   int now, next;
 
   __device__ __forceinline__ int fetch(const AttnArgs& a, int t) const {
     const int lane = threadIdx.x & 31;
-    if (t + lane / per_tile >= end) return -1;
-    return tab[a.page < kTile ? t * per_tile + lane
-                              : static_cast<int>(static_cast<uint32_t>(t + lane) * kTile /
-                                                 static_cast<uint32_t>(a.page))];
+    const uint32_t j = a.page < kTile
+                           ? static_cast<uint32_t>(t) * per_tile + lane
+                           : static_cast<uint32_t>(t + lane) * kTile / static_cast<uint32_t>(a.page);
+    return j < static_cast<uint32_t>(limit) ? tab[j] : -1;
   }
-  __device__ __forceinline__ void init(const AttnArgs& a, const int32_t* row, int t0, int t1) {
+  __device__ __forceinline__ void init(const AttnArgs& a, const int32_t* row, int t0, int len) {
     tab = row;
     per_tile = a.page < kTile ? kTile / a.page : 1;
     per_load = 32 / per_tile;
     t_at = t0;
-    end = t1;
+    limit = static_cast<int>((static_cast<uint32_t>(len) + a.page - 1) / a.page);
     now = fetch(a, t0);
     next = fetch(a, t0 + per_load);
   }
-  // This lane's page of full tile t (lanes below per_tile); t moves up by one.
-  // false: a page is not in the pool.
-  __device__ __forceinline__ bool get(const AttnArgs& a, int t, int& pg) {
+  // This lane's page of tile t (lanes below n, its pages with tokens); t moves
+  // up by one.  false: a page is not in the pool.
+  __device__ __forceinline__ bool get(const AttnArgs& a, int t, int here, int& pg, int& n) {
     if (t - t_at >= per_load) {
       t_at += per_load;
       now = next;
       next = fetch(a, t_at + per_load);
     }
     const int lane = threadIdx.x & 31;
+    n = per_tile == 1 ? 1 : (here + a.page - 1) / a.page;
     pg = __shfl_sync(0xffffffffu, now, ((t - t_at) * per_tile + lane) & 31);
-    return __all_sync(0xffffffffu, lane >= per_tile || (pg >= 0 && pg < a.n_pages));
+    return __all_sync(0xffffffffu, lane >= n || (pg >= 0 && pg < a.n_pages));
   }
 };
-
-// Whether a tile of the part may come by TMA: every token is there.  (A full
-// tile with a page outside the pool is the copy warps' as well.)
-__device__ __forceinline__ bool full_tile(const AttnArgs& a, const Walk& w, int t) {
-  return a.paged_tma && t < w.len / kTile;
-}
 
 __device__ __forceinline__ const int32_t* page_row(const AttnArgs& a, const Walk& w) {
   return w.e < a.P ? a.prefix_table + static_cast<long long>(w.e) * a.prefix_width
@@ -463,7 +470,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(&ctl->kv_full[s], kCopyWarps);
       mbar_init(&ctl->kv_empty[s], 1);
       mbar_init(&ctl->go[s], 1);
-      ctl->tma_fill[s] = -1;
+      ctl->tma_bar[s] = nullptr;
     }
     ctl->tma_q[0] = ctl->tma_q[1] = -1;
     for (int b = 0; b < 2; ++b) {
@@ -507,12 +514,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const uint32_t halves = a.D > 64 ? 2u : 1u;
   if (warp == kTmaWarp) {
     // ---------------------------------------------------------------- TMA
-    uint32_t tile = 0;
+    uint32_t tile = 0, go_used = 0;  // parity of each slot's `go`
     int item = 0;
     bool ok = true;
     PageIds ids;
     while (ok && w.part(a)) {
-      if (a.paged_tma) ids.init(a, page_row(a, w), w.t0, min(w.t1, w.len / kTile));
+      if (a.paged_tma) ids.init(a, page_row(a, w), w.t0, w.len);
       // the part's query rows: whole requests' heads of this KV head
       const int qb = item & 1;
       if (item >= 2 && !(ok = warp_wait(ctl, &ctl->q_empty[qb], (item / 2 + 1) & 1u, a.err))) break;
@@ -528,12 +535,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       ++item;
       for (int t = w.t0; ok && t < w.t1; ++t, ++tile) {
-        int pg = 0;
-        const bool mine = full_tile(a, w, t) && ids.get(a, t, pg);
+        const int here = min(w.len - t * kTile, kTile);
+        int pg = 0, n = 0;
+        const bool mine = a.paged_tma && ids.get(a, t, here, pg, n);
         const int row = a.page < kTile
                             ? 0
                             : static_cast<int>(static_cast<uint32_t>(t) * kTile %
                                                static_cast<uint32_t>(a.page));
+        const uint32_t box = (a.page < kTile ? a.page : kTile) * 128;  // of a page, 64 columns
         for (uint32_t kv = 0; kv < 2; ++kv) {
           const uint32_t f = 2 * tile + kv, slot = f % kSlots;
           if (f >= kSlots &&
@@ -541,30 +550,43 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             break;
           if (!mine) {
             if (lane == 0) mbar_arrive(&ctl->go[slot]);
+            go_used ^= 1u << slot;
             continue;
           }
-          if (kv == 0 && lane < 4) ctl->mask[tile % kMaskRing][lane] = 0xffffffffu;
-          __syncwarp();
-          if (lane == 0) {
-            ctl->tma_fill[slot] = static_cast<int>(f);
-            mbar_arrive_expect_tx(&ctl->kv_full[slot], halves * kHalf);
-            for (int i = 1; i < kCopyWarps; ++i) mbar_arrive(&ctl->kv_full[slot]);
+          // V of a tile that is not full goes to the copy warps when it has
+          // landed, for the zeros after its last token
+          uint64_t* bar = kv == 1 && here < kTile ? &ctl->go[slot] : &ctl->kv_full[slot];
+          if (kv == 0 && lane < 4) {
+            const int left = here - 32 * lane;
+            ctl->mask[tile % kMaskRing][lane] =
+                left >= 32 ? 0xffffffffu : (left > 0 ? (1u << left) - 1u : 0u);
           }
           __syncwarp();
-          uint8_t* dst = smem + kSmemKv + slot * kSlotBytes;
-          if (lane < ids.per_tile)
+          if (lane == 0) {
+            ctl->tma_phase[slot] =
+                (bar == &ctl->kv_full[slot] ? f / kSlots : go_used >> slot) & 1u;
+            ctl->tma_bar[slot] = bar;
+            mbar_arrive_expect_tx(bar, halves * n * box);
+            if (bar == &ctl->kv_full[slot])
+              for (int i = 1; i < kCopyWarps; ++i) mbar_arrive(bar);
+          }
+          __syncwarp();
+          if (bar == &ctl->go[slot]) go_used ^= 1u << slot;
+          uint8_t* dst = smem + kSmemKv + slot * kSlotBytes + lane * box;
+          if (lane < n)
             for (uint32_t i = 0; i < halves; ++i)
-              tma_load_4d(dst + i * kHalf + lane * a.page * 128, kv == 0 ? &tm_k : &tm_v,
-                          &ctl->kv_full[slot], 64 * i, w.head, row, pg);
+              tma_load_4d(dst + i * kHalf, kv == 0 ? &tm_k : &tm_v, bar, 64 * i, w.head, row, pg);
         }
       }
       w.next();
     }
   } else if (warp >= kCopyWarp0 && warp < kMmaWarp) {
     // ---------------------------------------------------------------- copies
-    // Tiles with fewer than 128 tokens or a page outside the pool, and all
-    // tiles where the page size does not fit: 16-byte copies that zero what
-    // is not there, 32 rows a warp.
+    // Tiles with a page outside the pool, and all tiles where the page size
+    // does not fit: 16-byte copies that zero what is not there, 32 rows a
+    // warp.  Of a partly filled tile that came by TMA: the zeros in V.  (Read
+    // by copies, such tiles cost 9,000 clocks: a warp's copies stop at every
+    // page that the TLB does not know, TMA's overlap.)
     const int cw = warp - kCopyWarp0;
     const int chunks = a.D / 8;
     uint32_t tile = 0, phases = 0;      // parity of each slot's `go`
@@ -582,18 +604,33 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     };
     while (ok && w.part(a)) {
       const int32_t* tab = page_row(a, w);
-      if (a.paged_tma) ids.init(a, tab, w.t0, min(w.t1, w.len / kTile));
+      if (a.paged_tma) ids.init(a, tab, w.t0, w.len);
       for (int t = w.t0; ok && t < w.t1; ++t, ++tile) {
-        if (full_tile(a, w, t)) {
-          int pg;
-          if (ids.get(a, t, pg)) continue;
-        }
         // K: the tokens there are (the other scores are never looked at).  V:
         // up to the product's depth, zeros where there is no token, as 0
         // times a stray NaN would be NaN.
         const uint32_t here = static_cast<uint32_t>(min(w.len - t * kTile, kTile));
+        const uint32_t deep = (here + 15) / 16 * 16;
+        int pg, unused;
+        if (a.paged_tma && ids.get(a, t, here, pg, unused)) {
+          if (here == kTile) continue;
+          const uint32_t slot = (2 * tile + 1) % kSlots;
+          cp_async_wait<0>();
+          announce(0);
+          if (!(ok = warp_wait(ctl, &ctl->go[slot], (phases >> slot) & 1u, a.err))) break;
+          phases ^= 1u << slot;
+          // rows here .. deep - 1, 16 lanes a row, every eighth row to a warp
+          const uint32_t dst = base + kSmemKv + slot * kSlotBytes;
+          const uint32_t c = lane & 15;
+          for (uint32_t i = here + 2 * cw + (lane >> 4); i < deep; i += 2 * kCopyWarps)
+            st_shared_zero16(dst + (c >> 3) * kHalf + i * 128 + (c & 7) * 16);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->kv_full[slot]);
+          continue;
+        }
         const uint32_t i = 32 * cw + lane;
-        int pg = -1;
+        pg = -1;
         uint32_t off = 0;
         if (i < here) {
           const uint32_t tok = static_cast<uint32_t>(t) * kTile + i;
@@ -607,7 +644,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         const uint32_t read = __ballot_sync(0xffffffffu, pg >= 0);
         const uint32_t fill_k = __ballot_sync(0xffffffffu, i < here);
-        const uint32_t fill_v = __ballot_sync(0xffffffffu, i < (here + 15) / 16 * 16);
+        const uint32_t fill_v = __ballot_sync(0xffffffffu, i < deep);
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           const uint32_t slot = (2 * tile + kv) % kSlots;
@@ -861,7 +898,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
     };
     for (int i = 0; i < kSlots; ++i)
-      if (ctl->tma_fill[i] >= 0) settle(&ctl->kv_full[i], (ctl->tma_fill[i] / kSlots) & 1);
+      if (ctl->tma_bar[i]) settle(ctl->tma_bar[i], ctl->tma_phase[i]);
     for (int i = 0; i < 2; ++i)
       if (ctl->tma_q[i] >= 0) settle(&ctl->q_full[i], (ctl->tma_q[i] >> 1) & 1);
   }

@@ -158,12 +158,12 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// 16-byte asynchronous copy global -> shared; the last 16 - bytes are zeros
-// (bytes = 0: nothing is read).  Per-thread groups.
-__device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(src),
-               "r"(bytes)
-               : "memory");
+// 16-byte asynchronous copy global -> shared, in per-thread groups.
+__device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void st_shared_zero16(uint32_t smem_dst) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(smem_dst), "r"(0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");

@@ -64,7 +64,7 @@ constexpr int kMaskRing = 8;
 constexpr uint32_t kSmemQ = 0;                             // two buffers
 constexpr uint32_t kSmemKv = kSmemQ + 2 * kSlotBytes;
 constexpr uint32_t kSmemCtl = kSmemKv + kSlots * kSlotBytes;
-constexpr uint32_t kAttnSmem = kSmemCtl + 1024 + 1024;     // control block, alignment
+constexpr uint32_t kAttnSmem = kSmemCtl + 2048 + 1024;     // control block, alignment
 constexpr int kLag = 3;         // copied fills issued but not yet announced
 // TMEM columns of a group: O, then S; P takes the first half of S's
 constexpr uint32_t kColO = 0, kColS = 128, kColGroup = 256;
@@ -83,13 +83,26 @@ struct AttnArgs {
   float scale;  // times log2 e
   int n_pages, page, prefix_width, P, width, B, Hq, Hkv, D, rep, ctas;
   int row_tile;       // query rows per prompt item: whole requests, at most 128
-  int paged_tma;      // pages and tiles fit each other: full tiles come by TMA
+  int paged_tma;      // pages and tiles fit each other: tiles come by TMA
+  // A K or V tile in its slot: 16 groups of 8 rows x 128 bytes (64 columns),
+  // group_bytes apart, the second 64 columns half_bytes behind the first.
+  // `fold` says how a page's box is addressed (kFold*).
+  uint32_t group_bytes, half_bytes;
+  int fold;
   // workspace
   long long* starts;  // [P + B + 1] first tile of each entry
   int32_t* clen;      // [P + B] clean lengths
   int32_t* cu;        // [P + 1] clean offsets
   float *o_base, *o_extra;    // [2][groups][B * Hq][D], [ctas][groups][128][D]
   float2 *ml_base, *ml_extra;
+};
+
+// How the cache's axes fold into the five of a tensor map, innermost first:
+// 64 columns, 8 rows, ..., groups of 8 rows, ...
+enum Fold {
+  kFoldNone,       // ..., heads, groups, pages: a box for each 64 columns
+  kFoldHeads,      // heads' 64-column halves in a row: (head, half), groups, pages
+  kFoldPages       // halves, groups, (page, head)
 };
 
 struct AttnLayout {
@@ -250,26 +263,46 @@ struct Walk {
     }
   }
   __device__ __forceinline__ void next() { x += taken; }
-  // the softmax group of tile t: alternating, and from item to item
-  __device__ __forceinline__ int group(int t) const { return (t + head + e) & 1; }
-  // request and query head of row r of the part
-  __device__ __forceinline__ void row(const AttnArgs& a, int r, int& b, int& h) const {
-    if (e < a.P) {
-      const int i = row_tile * a.row_tile + r;
-      b = a.cu[e] + i / a.rep;
-      h = head * a.rep + i % a.rep;
-    } else {
-      b = e - a.P;
-      h = head * a.rep + r;
-    }
-  }
 };
 
+// What the other roles need of a part (t0 = t1: there are no more).  The TMA
+// warp alone walks the line and writes this down.
+struct PartInfo {
+  int e, head, row_tile, t0, t1, len, rows, first;
+};
+// What the copy warps are asked for, in order; a job holds a slot of the ring
+// until it is done, so there are never more than slots.
+struct CopyJob {
+  int slot, kind, e, head, t, here, mask;  // mask: place of the tile's bits
+};
+enum { kJobK, kJobV, kJobZeros, kJobEnd };
+constexpr int kPartRing = 8, kJobRing = 8;
+
+// The softmax group of a part's tile t: alternating, and from item to item.
+__device__ __forceinline__ int tile_group(const PartInfo& w, int t) {
+  return (t + w.head + w.e) & 1;
+}
+// Request and query head of row r of a part.
+__device__ __forceinline__ void part_row(const AttnArgs& a, const PartInfo& w, int r, int& b,
+                                         int& h) {
+  if (w.e < a.P) {
+    const int i = w.row_tile * a.row_tile + r;
+    b = a.cu[w.e] + i / a.rep;
+    h = w.head * a.rep + i % a.rep;
+  } else {
+    b = w.e - a.P;
+    h = w.head * a.rep + r;
+  }
+}
+
 struct AttnCtl {
-  uint64_t kv_full[kSlots], kv_empty[kSlots], go[kSlots];
+  uint64_t kv_full[kSlots], kv_empty[kSlots], landed[kSlots];
   uint64_t q_full[2], q_empty[2], s_full[kGroups], p_full[kGroups], pv_done[kGroups];
   uint64_t o_free[kGroups], drain;
+  uint64_t part_full[kPartRing], part_empty[kPartRing], job_full[kJobRing];
   uint32_t mask[kMaskRing][4];
+  PartInfo part[kPartRing];
+  CopyJob job[kJobRing];
   uint32_t tmem;
   int abort;
   // what a TMA copy was last issued for: a slot's barrier and its phase, a
@@ -278,22 +311,34 @@ struct AttnCtl {
   uint32_t tma_phase[kSlots];
   int tma_q[2];
 };
-static_assert(sizeof(AttnCtl) <= 1024, "control block");
+static_assert(sizeof(AttnCtl) <= 2048, "control block");
 
 __device__ __forceinline__ void attn_abort(AttnCtl* c, int* err) {
   *const_cast<volatile int*>(&c->abort) = 1;
   if (err) atomicOr(err, RZ_DEVERR_TIMEOUT);
 }
-// One lane waits, the verdict is the warp's.
-__device__ __forceinline__ bool warp_wait(AttnCtl* c, uint64_t* bar, uint32_t parity, int* err) {
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) {
-    ok = mbar_wait<true>(bar, parity, const_cast<volatile int*>(&c->abort), kWaitLimitNs) ? 1 : 0;
-    if (!ok) attn_abort(c, err);
+// Waits are bounded (2 s).  What follows a first failed test is one piece of
+// code for all of them: inlined at every wait it made the roles' loops too
+// long for the instruction cache.
+__device__ __noinline__ bool attn_wait_slow(AttnCtl* c, uint32_t bar, uint32_t parity, int* err) {
+  const volatile int* abort = const_cast<volatile int*>(&c->abort);
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      attn_abort(c, err);
+      return false;
+    }
   }
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  __syncwarp();
-  return ok != 0;
+  return true;
+}
+__device__ __forceinline__ bool lane_wait(AttnCtl* c, uint64_t* bar, uint32_t parity, int* err) {
+  const uint32_t at = smem_u32(bar);
+  return mbar_try_wait(at, parity) || attn_wait_slow(c, at, parity, err);
+}
+// A whole warp; the verdict is the warp's.
+__device__ __forceinline__ bool warp_wait(AttnCtl* c, uint64_t* bar, uint32_t parity, int* err) {
+  return __all_sync(0xffffffffu, lane_wait(c, bar, parity, err));
 }
 
 // 32 rows of a tile into their swizzled place: `row` is the start of this
@@ -303,27 +348,30 @@ __device__ __forceinline__ bool warp_wait(AttnCtl* c, uint64_t* bar, uint32_t pa
 // the exchanges of row addresses overlap: one by one they take 106 clocks an
 // iteration.
 template <int kLanes>
-__device__ __forceinline__ void load_rows_n(uint32_t dst, const uint8_t* row, uint32_t read,
-                                            uint32_t fill, int w, int chunks) {
+__device__ __forceinline__ void load_rows_n(const AttnArgs& a, uint32_t dst, const uint8_t* row,
+                                            uint32_t read, uint32_t fill, int w) {
   const int lane = threadIdx.x & 31;
   constexpr int kStep = 32 / kLanes;
   const int c = lane % kLanes, sub = lane / kLanes;
-  const bool mine = c < chunks;
-  const uint32_t base = dst + (c >> 3) * kHalf + (32 * w + sub) * 128;
+  const bool mine = c < a.D / 8;
+  const uint32_t base = dst + (c >> 3) * a.half_bytes + 4 * w * a.group_bytes;
+  const auto place = [&](int r) {
+    return base + (r >> 3) * a.group_bytes + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4);
+  };
 #pragma unroll
   for (int i = 0; i < kLanes; ++i) {
     const int r = sub + kStep * i;
     const uint8_t* p = reinterpret_cast<const uint8_t*>(
         __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r));
     if (mine && ((read >> r) & 1u))
-      cp_async16(base + kStep * i * 128 + (((c & 7) ^ (r & 7)) << 4), p + 16 * c);
+      cp_async16(place(r), p + 16 * c);
   }
   if (fill & ~read) {
 #pragma unroll 1
     for (int i = 0; i < kLanes; ++i) {
       const int r = sub + kStep * i;
       if (mine && ((fill & ~read) >> r) & 1u)
-        st_shared_zero16(base + kStep * i * 128 + (((c & 7) ^ (r & 7)) << 4));
+        st_shared_zero16(place(r));
     }
   }
 }
@@ -369,9 +417,9 @@ struct PageIds {
   }
 };
 
-__device__ __forceinline__ const int32_t* page_row(const AttnArgs& a, const Walk& w) {
-  return w.e < a.P ? a.prefix_table + static_cast<long long>(w.e) * a.prefix_width
-                   : a.table + static_cast<long long>(w.e - a.P) * a.width;
+__device__ __forceinline__ const int32_t* page_row(const AttnArgs& a, int e) {
+  return e < a.P ? a.prefix_table + static_cast<long long>(e) * a.prefix_width
+                 : a.table + static_cast<long long>(e - a.P) * a.width;
 }
 
 template <class E>
@@ -469,7 +517,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&ctl->kv_full[s], kCopyWarps);
       mbar_init(&ctl->kv_empty[s], 1);
-      mbar_init(&ctl->go[s], 1);
+      mbar_init(&ctl->landed[s], 1);
       ctl->tma_bar[s] = nullptr;
     }
     ctl->tma_q[0] = ctl->tma_q[1] = -1;
@@ -483,6 +531,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(&ctl->pv_done[g], 1);
       mbar_init(&ctl->o_free[g], kGroupWarps);
     }
+    for (int i = 0; i < kPartRing; ++i) {
+      mbar_init(&ctl->part_full[i], 1);
+      mbar_init(&ctl->part_empty[i], kGroups * kGroupWarps);
+    }
+    for (int i = 0; i < kJobRing; ++i) mbar_init(&ctl->job_full[i], 1);
     mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -505,30 +558,59 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   grid_dep_launch();
   grid_dep_wait();  // the plan
 
-  Walk w;
-  w.init(a, blockIdx.x);
-
   // Fill f of the ring is K of tile f / 2, then its V.  The TMA warp claims
-  // every slot in order; a fill that is not its own it hands to the copy
-  // warps through the slot's `go`.
+  // every slot in order; a fill that is not its own is a job for the copy
+  // warps.
   const uint32_t halves = a.D > 64 ? 2u : 1u;
   if (warp == kTmaWarp) {
     // ---------------------------------------------------------------- TMA
-    uint32_t tile = 0, go_used = 0;  // parity of each slot's `go`
+    Walk w;
+    w.init(a, blockIdx.x);
+    PageIds ids;
+    uint32_t tile = 0, landed = 0, jobs = 0;  // landed: parity of each slot's
     int item = 0;
     bool ok = true;
-    PageIds ids;
+    const auto give = [&](int slot, int kind, int t, int here) {
+      if (lane == 0) {
+        CopyJob& j = ctl->job[jobs % kJobRing];
+        j.slot = slot;
+        j.kind = kind;
+        j.e = w.e;
+        j.head = w.head;
+        j.t = t;
+        j.here = here;
+        j.mask = tile % kMaskRing;
+        mbar_arrive(&ctl->job_full[jobs % kJobRing]);
+      }
+      ++jobs;
+    };
+    const auto part_free = [&]() {  // the place of part `item`
+      return item < kPartRing || warp_wait(ctl, &ctl->part_empty[item % kPartRing],
+                                           (item / kPartRing + 1) & 1u, a.err);
+    };
     while (ok && w.part(a)) {
-      if (a.paged_tma) ids.init(a, page_row(a, w), w.t0, w.len);
-      // the part's query rows: whole requests' heads of this KV head
+      if (!(ok = part_free())) break;
+      if (a.paged_tma) ids.init(a, page_row(a, w.e), w.t0, w.len);
       const int qb = item & 1;
       if (item >= 2 && !(ok = warp_wait(ctl, &ctl->q_empty[qb], (item / 2 + 1) & 1u, a.err))) break;
       if (lane == 0) {
+        PartInfo& pi = ctl->part[item % kPartRing];
+        pi.e = w.e;
+        pi.head = w.head;
+        pi.row_tile = w.row_tile;
+        pi.t0 = w.t0;
+        pi.t1 = w.t1;
+        pi.len = w.len;
+        pi.rows = w.rows;
+        pi.first = w.first;
+        mbar_arrive(&ctl->part_full[item % kPartRing]);
+        // the part's query rows: whole requests' heads of this KV head
         const bool group = w.e < a.P;
         const uint32_t rows = group ? a.row_tile : a.rep;
         mbar_arrive_expect_tx(&ctl->q_full[qb], rows * 128 * halves);
         ctl->tma_q[qb] = item;
         const int b = group ? a.cu[w.e] + w.row_tile * (a.row_tile / a.rep) : w.e - a.P;
+#pragma unroll 1
         for (uint32_t i = 0; i < halves; ++i)
           tma_load_3d(smem + kSmemQ + qb * kSlotBytes + i * kHalf, group ? &tm_q_group : &tm_q_own,
                       &ctl->q_full[qb], 64 * i, w.head * a.rep, b);
@@ -538,24 +620,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int here = min(w.len - t * kTile, kTile);
         int pg = 0, n = 0;
         const bool mine = a.paged_tma && ids.get(a, t, here, pg, n);
-        const int row = a.page < kTile
-                            ? 0
-                            : static_cast<int>(static_cast<uint32_t>(t) * kTile %
-                                               static_cast<uint32_t>(a.page));
-        const uint32_t box = (a.page < kTile ? a.page : kTile) * 128;  // of a page, 64 columns
+        // in groups of 8 rows: where the tile begins in its page, a box
+        const int row8 = a.page < kTile
+                             ? 0
+                             : static_cast<int>(static_cast<uint32_t>(t) * kTile %
+                                                static_cast<uint32_t>(a.page)) / 8;
+        const uint32_t box8 = (a.page < kTile ? a.page : kTile) / 8;
+#pragma unroll 1
         for (uint32_t kv = 0; kv < 2; ++kv) {
           const uint32_t f = 2 * tile + kv, slot = f % kSlots;
           if (f >= kSlots &&
               !(ok = warp_wait(ctl, &ctl->kv_empty[slot], (f / kSlots + 1) & 1u, a.err)))
             break;
           if (!mine) {
-            if (lane == 0) mbar_arrive(&ctl->go[slot]);
-            go_used ^= 1u << slot;
+            give(slot, kv == 0 ? kJobK : kJobV, t, here);
             continue;
           }
           // V of a tile that is not full goes to the copy warps when it has
           // landed, for the zeros after its last token
-          uint64_t* bar = kv == 1 && here < kTile ? &ctl->go[slot] : &ctl->kv_full[slot];
+          const bool zeros = kv == 1 && here < kTile;
+          uint64_t* bar = zeros ? &ctl->landed[slot] : &ctl->kv_full[slot];
           if (kv == 0 && lane < 4) {
             const int left = here - 32 * lane;
             ctl->mask[tile % kMaskRing][lane] =
@@ -563,22 +647,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           __syncwarp();
           if (lane == 0) {
-            ctl->tma_phase[slot] =
-                (bar == &ctl->kv_full[slot] ? f / kSlots : go_used >> slot) & 1u;
+            ctl->tma_phase[slot] = (zeros ? landed >> slot : f / kSlots) & 1u;
             ctl->tma_bar[slot] = bar;
-            mbar_arrive_expect_tx(bar, halves * n * box);
-            if (bar == &ctl->kv_full[slot])
-              for (int i = 1; i < kCopyWarps; ++i) mbar_arrive(bar);
+            mbar_arrive_expect_tx(bar, halves * n * box8 * 1024);
+            if (!zeros) mbar_arrive_n(bar, kCopyWarps - 1);
           }
           __syncwarp();
-          if (bar == &ctl->go[slot]) go_used ^= 1u << slot;
-          uint8_t* dst = smem + kSmemKv + slot * kSlotBytes + lane * box;
-          if (lane < n)
-            for (uint32_t i = 0; i < halves; ++i)
-              tma_load_4d(dst + i * kHalf, kv == 0 ? &tm_k : &tm_v, bar, 64 * i, w.head, row, pg);
+          if (lane < n) {
+            uint8_t* dst = smem + kSmemKv + slot * kSlotBytes + lane * box8 * a.group_bytes;
+            const CUtensorMap* tm = kv == 0 ? &tm_k : &tm_v;
+            if (a.fold == kFoldHeads) {
+              tma_load_5d(dst, tm, bar, 0, 0, 2 * w.head, row8, pg);
+            } else if (a.fold == kFoldPages) {
+              tma_load_5d(dst, tm, bar, 0, 0, 0, row8, pg * a.Hkv + w.head);
+            } else {
+#pragma unroll 1
+              for (uint32_t i = 0; i < halves; ++i)
+                tma_load_5d(dst + i * a.half_bytes, tm, bar, 64 * i, 0, w.head, row8, pg);
+            }
+          }
+          if (zeros) {
+            give(slot, kJobZeros, t, here);
+            landed ^= 1u << slot;
+          }
         }
       }
       w.next();
+    }
+    // no more: whoever waits for a part or a job is told
+    give(0, kJobEnd, 0, 0);
+    if (ok && part_free() && lane == 0) {
+      PartInfo& pi = ctl->part[item % kPartRing];
+      pi.t0 = pi.t1 = 0;
+      mbar_arrive(&ctl->part_full[item % kPartRing]);
     }
   } else if (warp >= kCopyWarp0 && warp < kMmaWarp) {
     // ---------------------------------------------------------------- copies
@@ -588,95 +689,80 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // by copies, such tiles cost 9,000 clocks: a warp's copies stop at every
     // page that the TLB does not know, TMA's overlap.)
     const int cw = warp - kCopyWarp0;
-    const int chunks = a.D / 8;
-    uint32_t tile = 0, phases = 0;      // parity of each slot's `go`
+    uint32_t landed = 0;                // parity of each slot's
     uint32_t queue = 0;                 // slots issued and not announced, 4 bits each
     int queued = 0;
-    bool ok = true;
     int bad = 0;
-    PageIds ids;
     const auto announce = [&](int left) {  // all but `left`; their copies are done
       fence_proxy_async_smem();
       __syncwarp();
+#pragma unroll 1
       for (; queued > left; --queued) {
         if (lane == 0) mbar_arrive(&ctl->kv_full[(queue >> (4 * (queued - 1))) & 15u]);
       }
     };
-    while (ok && w.part(a)) {
-      const int32_t* tab = page_row(a, w);
-      if (a.paged_tma) ids.init(a, tab, w.t0, w.len);
-      for (int t = w.t0; ok && t < w.t1; ++t, ++tile) {
-        // K: the tokens there are (the other scores are never looked at).  V:
-        // up to the product's depth, zeros where there is no token, as 0
-        // times a stray NaN would be NaN.
-        const uint32_t here = static_cast<uint32_t>(min(w.len - t * kTile, kTile));
-        const uint32_t deep = (here + 15) / 16 * 16;
-        int pg, unused;
-        if (a.paged_tma && ids.get(a, t, here, pg, unused)) {
-          if (here == kTile) continue;
-          const uint32_t slot = (2 * tile + 1) % kSlots;
-          cp_async_wait<0>();
-          announce(0);
-          if (!(ok = warp_wait(ctl, &ctl->go[slot], (phases >> slot) & 1u, a.err))) break;
-          phases ^= 1u << slot;
-          // rows here .. deep - 1, 16 lanes a row, every eighth row to a warp
-          const uint32_t dst = base + kSmemKv + slot * kSlotBytes;
-          const uint32_t c = lane & 15;
-          for (uint32_t i = here + 2 * cw + (lane >> 4); i < deep; i += 2 * kCopyWarps)
-            st_shared_zero16(dst + (c >> 3) * kHalf + i * 128 + (c & 7) * 16);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->kv_full[slot]);
-          continue;
-        }
-        const uint32_t i = 32 * cw + lane;
-        pg = -1;
-        uint32_t off = 0;
-        if (i < here) {
-          const uint32_t tok = static_cast<uint32_t>(t) * kTile + i;
-          const uint32_t j = tok / static_cast<uint32_t>(a.page);
-          off = tok - j * static_cast<uint32_t>(a.page);
-          pg = tab[j];
-          if (pg < 0 || pg >= a.n_pages) {
-            pg = -1;
-            bad = RZ_DEVERR_PAGES;
-          }
-        }
-        const uint32_t read = __ballot_sync(0xffffffffu, pg >= 0);
-        const uint32_t fill_k = __ballot_sync(0xffffffffu, i < here);
-        const uint32_t fill_v = __ballot_sync(0xffffffffu, i < deep);
+    for (uint32_t n = 0;; ++n) {
+      uint64_t* bar = &ctl->job_full[n % kJobRing];
+      const uint32_t ph = (n / kJobRing) & 1u;
+      if (queued > 0 && !__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), ph))) {
+        // nothing to do: what has been issued may be waited for by others
+        cp_async_wait<0>();
+        announce(0);
+      }
+      if (!warp_wait(ctl, bar, ph, a.err)) break;
+      const CopyJob job = ctl->job[n % kJobRing];
+      if (job.kind == kJobEnd) break;
+      const uint32_t dst = base + kSmemKv + job.slot * kSlotBytes;
+      // K: the tokens there are (the other scores are never looked at).  V:
+      // up to the product's depth, zeros where there is no token, as 0 times
+      // a stray NaN would be NaN.
+      const uint32_t here = static_cast<uint32_t>(job.here);
+      const uint32_t deep = (here + 15) / 16 * 16;
+      if (job.kind == kJobZeros) {
+        if (!warp_wait(ctl, &ctl->landed[job.slot], (landed >> job.slot) & 1u, a.err)) break;
+        landed ^= 1u << job.slot;
+        // rows here .. deep - 1, 16 lanes a row, every eighth row to a warp
+        const uint32_t c = lane & 15;
 #pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t slot = (2 * tile + kv) % kSlots;
-          uint64_t* bar = &ctl->go[slot];
-          const uint32_t ph = (phases >> slot) & 1u;
-          if (!__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), ph))) {
-            // nothing to do: what has been issued may be waited for by others
-            cp_async_wait<0>();
-            announce(0);
-            if (!(ok = warp_wait(ctl, bar, ph, a.err))) break;
-          }
-          phases ^= 1u << slot;
-          if (kv == 0 && lane == 0) ctl->mask[tile % kMaskRing][cw] = read;
-          const uint8_t* row = static_cast<const uint8_t*>(kv == 0 ? a.k : a.v);
-          const long long* st = kv == 0 ? a.ks : a.vs;
-          if (pg >= 0)
-            row += 2 * (pg * st[0] + static_cast<long long>(off) * st[1] + w.head * st[2]);
-          const uint32_t dst = base + kSmemKv + slot * kSlotBytes;
-          const uint32_t fill = kv == 0 ? fill_k : fill_v;
-          if (fill != 0) {
-            if (chunks > 8) load_rows_n<16>(dst, row, read, fill, cw, chunks);
-            else load_rows_n<8>(dst, row, read, fill, cw, chunks);
-          }
-          cp_async_commit();
-          queue = queue << 4 | slot;
-          if (++queued > kLag) {
-            cp_async_wait<kLag>();
-            announce(kLag);
-          }
+        for (uint32_t i = here + 2 * cw + (lane >> 4); i < deep; i += 2 * kCopyWarps)
+          if (c < 8 * halves)
+            st_shared_zero16(dst + (c >> 3) * a.half_bytes + (i >> 3) * a.group_bytes +
+                             (i & 7) * 128 + (c & 7) * 16);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->kv_full[job.slot]);
+        continue;
+      }
+      const bool is_k = job.kind == kJobK;
+      const uint32_t i = 32 * cw + lane;
+      bool there = false;
+      const uint8_t* row = static_cast<const uint8_t*>(is_k ? a.k : a.v);
+      if (i < here) {
+        const uint32_t tok = static_cast<uint32_t>(job.t) * kTile + i;
+        const uint32_t j = tok / static_cast<uint32_t>(a.page);
+        const int pg = page_row(a, job.e)[j];
+        there = pg >= 0 && pg < a.n_pages;
+        if (there) {
+          const long long* st = is_k ? a.ks : a.vs;
+          const long long off = tok - j * static_cast<uint32_t>(a.page);
+          row += 2 * (pg * st[0] + off * st[1] + job.head * st[2]);
+        } else {
+          bad = RZ_DEVERR_PAGES;
         }
       }
-      w.next();
+      const uint32_t read = __ballot_sync(0xffffffffu, there);
+      const uint32_t fill = __ballot_sync(0xffffffffu, i < (is_k ? here : deep));
+      if (is_k && lane == 0) ctl->mask[job.mask][cw] = read;
+      if (fill != 0) {
+        if (a.D > 64) load_rows_n<16>(a, dst, row, read, fill, cw);
+        else load_rows_n<8>(a, dst, row, read, fill, cw);
+      }
+      cp_async_commit();
+      queue = queue << 4 | static_cast<uint32_t>(job.slot);
+      if (++queued > kLag) {
+        cp_async_wait<kLag>();
+        announce(kLag);
+      }
     }
     cp_async_wait<0>();
     announce(0);
@@ -690,105 +776,91 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const uint32_t idesc_s = (1u << 4) | fmt | ((kTile >> 4) << 24);  // and N / 8 << 17
       const uint32_t idesc_o = (1u << 4) | fmt | (1u << 16) | ((2 * depth) << 17) |
                                ((kTile >> 4) << 24);
-      const volatile int* abort = const_cast<volatile int*>(&ctl->abort);
+      const uint64_t desc_k = sdesc_sw128(base + kSmemKv, 16u, a.group_bytes);
+      const uint64_t desc_v = sdesc_sw128(base + kSmemKv, a.half_bytes, a.group_bytes);
+      const uint64_t desc_q = sdesc_sw128(base + kSmemQ, 16u, 1024u);
+      const uint32_t step_k = (a.half_bytes >> 4) - 6, step_q = (kHalf >> 4) - 6;
       bool ok = true;
       uint32_t tile = 0;                      // S issued
-      uint32_t p_used = 0, o_used[kGroups] = {0, 0};  // p_full phases; parts begun
-      int item = 0;
+      uint32_t p_used = 0, o_used = 0, o_begun = 0;  // phases, a bit for each group
       bool pend = false, pend_first = false;  // the tile whose P V is due
       int pend_k = 0, pend_g = 0;             // its tokens / 16, its group
       const auto pv = [&]() {
         const uint32_t f = 2 * tile - 1, slot = f % kSlots;  // V of tile - 1
         const int g = pend_g;
-        if (!mbar_wait(&ctl->kv_full[slot], (f / kSlots) & 1u, abort, kWaitLimitNs) ||
-            !mbar_wait(&ctl->p_full[g], (p_used >> g) & 1u, abort, kWaitLimitNs))
+        if (!lane_wait(ctl, &ctl->kv_full[slot], (f / kSlots) & 1u, a.err) ||
+            !lane_wait(ctl, &ctl->p_full[g], (p_used >> g) & 1u, a.err))
           return false;
         p_used ^= 1u << g;
         if (pend_first) {
-          const uint32_t used = g == 0 ? o_used[0]++ : o_used[1]++;
-          if (used > 0 && !mbar_wait(&ctl->o_free[g], (used - 1) & 1u, abort, kWaitLimitNs))
-            return false;
+          if ((o_begun >> g) & 1u) {
+            if (!lane_wait(ctl, &ctl->o_free[g], (o_used >> g) & 1u, a.err)) return false;
+            o_used ^= 1u << g;
+          }
+          o_begun |= 1u << g;
         }
         tc_fence_after();
-        const uint64_t v = sdesc_sw128(base + kSmemKv + slot * kSlotBytes, kHalf, 1024u);
-        const uint32_t o = tmem + g * kColGroup + kColO, p = tmem + g * kColGroup + kColS;
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          if (k < pend_k)
-            umma_f16_ts(o, p + 8 * k, v + (2048u * k >> 4), idesc_o,
-                        (pend_first && k == 0) ? 0u : 1u);
+        uint64_t v = desc_v + slot * (kSlotBytes >> 4);
+        const uint32_t o = tmem + g * kColGroup + kColO;
+        uint32_t p = tmem + g * kColGroup + kColS;
+#pragma unroll 1
+        for (int k = 0; k < pend_k; ++k) {
+          umma_f16_ts(o, p, v, idesc_o, (pend_first && k == 0) ? 0u : 1u);
+          p += 8;
+          v += a.group_bytes >> 3;
+        }
         umma_commit(&ctl->kv_empty[slot]);
         umma_commit(&ctl->pv_done[g]);
+        pend = false;
         return true;
       };
-      while (true) {
-        const bool more = ok && w.part(a);
-        if (!more && !(ok && pend)) break;
-        const int t_end = more ? w.t1 : 1;
-        uint64_t q = 0;
-        if (more) {
-          q = sdesc_sw128(base + kSmemQ + (item & 1) * kSlotBytes, 16u, 1024u);
-          if (!mbar_wait(&ctl->q_full[item & 1], (item >> 1) & 1u, abort, kWaitLimitNs)) {
-            ok = false;
-            break;
+      for (int item = 0; ok; ++item) {
+        PartInfo w;
+        w.t0 = w.t1 = 0;
+        if (lane_wait(ctl, &ctl->part_full[item % kPartRing], (item / kPartRing) & 1u, a.err))
+          w = ctl->part[item % kPartRing];
+        else
+          ok = false;
+        if (w.t0 == w.t1) break;
+        if (!(ok = lane_wait(ctl, &ctl->q_full[item & 1], (item >> 1) & 1u, a.err))) break;
+#pragma unroll 1
+        for (int t = w.t0; t < w.t1; ++t) {
+          const uint32_t f = 2 * tile, slot = f % kSlots;
+          if (!(ok = lane_wait(ctl, &ctl->kv_full[slot], (f / kSlots) & 1u, a.err))) break;
+          const int g = tile_group(w, t);
+          // S[g] is free: P V of the group's tile before, issued earlier in
+          // this order, is what reads it last.  That may be the one still due
+          // (two parts, a tile each): then it goes first.
+          const bool before = pend && pend_g == g;
+          if (before && !(ok = pv())) break;
+          tc_fence_after();
+          const int n16 = (min(w.len - t * kTile, kTile) + 15) / 16;  // tokens / 16
+          const uint32_t idesc = idesc_s | (static_cast<uint32_t>(2 * n16) << 17);
+          uint64_t dk = desc_k + slot * (kSlotBytes >> 4);
+          uint64_t dq = desc_q + (item & 1) * (kSlotBytes >> 4);
+          const uint32_t sc = tmem + g * kColGroup + kColS;
+#pragma unroll 1
+          for (uint32_t k = 0; k < depth; ++k) {
+            umma_bf16(sc, dq, dk, idesc, k > 0 ? 1u : 0u);
+            dq += k == 3 ? step_q : 2u;
+            dk += k == 3 ? step_k : 2u;
           }
-        }
-        // (after the last part: one more turn, for the last tile's P V)
-        for (int t = more ? w.t0 : 0; t < t_end; ++t) {
-          if (more) {
-            const uint32_t f = 2 * tile, slot = f % kSlots;
-            if (!mbar_wait(&ctl->kv_full[slot], (f / kSlots) & 1u, abort, kWaitLimitNs)) {
-              ok = false;
-              break;
-            }
-            // S[g] is free: P V of the group's tile before, issued earlier in
-            // this order, is what reads it last
-            tc_fence_after();
-            const int g = w.group(t);
-            const int n16 = (min(w.len - t * kTile, kTile) + 15) / 16;  // tokens / 16
-            const uint32_t idesc = idesc_s | (static_cast<uint32_t>(2 * n16) << 17);
-            const uint64_t k0 = sdesc_sw128(base + kSmemKv + slot * kSlotBytes, 16u, 1024u);
-            const uint32_t sc = tmem + g * kColGroup + kColS;
-            // the group's tile before may be the one whose P V is due (two
-            // parts of one tile each): then it goes first
-            if (pend && pend_g == g) {
-              if (!pv()) {
-                ok = false;
-                break;
-              }
-              pend = false;
-            }
-#pragma unroll
-            for (uint32_t k = 0; k < kMaxD / 16; ++k) {
-              const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32u) >> 4;
-              if (k < depth) umma_bf16(sc, q + off, k0 + off, idesc, k > 0 ? 1u : 0u);
-            }
-            umma_commit(&ctl->kv_empty[slot]);
-            umma_commit(&ctl->s_full[g]);
-            if (t == w.t1 - 1) umma_commit(&ctl->q_empty[item & 1]);
-            if (pend && !pv()) {
-              ok = false;
-              break;
-            }
-            pend = true;
-            pend_first = t < w.t0 + 2;  // the group's first tile of the part
-            pend_k = n16;
-            pend_g = g;
-            ++tile;
-          } else {
-            ok = pv();
-            pend = false;
-          }
-        }
-        if (more) {
-          ++item;
-          w.next();
+          umma_commit(&ctl->kv_empty[slot]);
+          umma_commit(&ctl->s_full[g]);
+          if (t == w.t1 - 1) umma_commit(&ctl->q_empty[item & 1]);
+          if (pend && !(ok = pv())) break;
+          pend = true;
+          pend_first = t < w.t0 + 2;  // the group's first tile of the part
+          pend_k = n16;
+          pend_g = g;
+          ++tile;
         }
       }
+      if (ok && pend) ok = pv();
       if (!ok) attn_abort(ctl, a.err);
       // no MMA is in flight when TMEM is freed
       umma_commit(&ctl->drain);
-      if (!mbar_wait(&ctl->drain, 0, abort, kWaitLimitNs) && !*abort) attn_abort(ctl, a.err);
+      if (!lane_wait(ctl, &ctl->drain, 0, a.err)) attn_abort(ctl, a.err);
     }
   } else {
     // ---------------------------------------------------------------- softmax
@@ -801,52 +873,60 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     soft.zero = a.scale == 0.f;
     soft.general = soft.flip || soft.zero;
     soft.sl = soft.zero ? 1.f : fabsf(a.scale);
-    uint32_t tile0 = 0;             // tiles of the parts before
+    uint32_t tile0 = 0;                // tiles of the parts before
     uint32_t s_used = 0, pv_used = 0;  // phases
-    bool ok = true;
-    while (ok && w.part(a)) {
+    for (int item = 0;; ++item) {
+      if (!warp_wait(ctl, &ctl->part_full[item % kPartRing], (item / kPartRing) & 1u, a.err)) break;
+      const PartInfo w = ctl->part[item % kPartRing];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->part_empty[item % kPartRing]);
+      if (w.t0 == w.t1) break;
       const bool live = quad * 32 < w.rows;
-      const int first = w.t0 + (w.group(w.t0) != g);  // this group's tiles: first, first + 2, ...
+      const int first = w.t0 + (tile_group(w, w.t0) != g);  // this group's: first, first + 2, ...
+      bool ok = true;
       float m = -INFINITY, l = 0.f;
+#pragma unroll 1
       for (int t = first; t < w.t1; t += 2) {
         if (!(ok = warp_wait(ctl, &ctl->s_full[g], s_used & 1u, a.err))) break;
         ++s_used;
         tc_fence_after();
+        float top = -INFINITY;
+        bool grow = false;
+        int here = 0;
         if (live) {
           const uint32_t tile = tile0 + (t - w.t0);
 #pragma unroll
           for (int i = 0; i < 4; ++i) soft.bits[i] = ctl->mask[tile % kMaskRing][i];
-          const int here = min(w.len - t * kTile, kTile);
-          const float top = tile_max(sc, soft);
-          const bool grow = top > m + kGrow || (m == -INFINITY && top > m);
-          if (t > first) {
-            // the group's P V before this one: O may be touched
-            if (!(ok = warp_wait(ctl, &ctl->pv_done[g], pv_used & 1u, a.err))) break;
-            ++pv_used;
-            if (__any_sync(0xffffffffu, grow && r < w.rows)) {
-              // O of the tiles before moves to the new reference
-              tc_fence_after();
-              const float f = grow ? (m == -INFINITY ? 0.f : ex2_approx(m - top)) : 1.f;
-#pragma unroll 1
-              for (int i = 0; i < a.D; i += 32) {
-                uint32_t o[32];
-                tmem_ld32(lanes + kColO + i, o);
-                tmem_ld_wait();
-#pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                tmem_st32(lanes + kColO + i, o);
-              }
-              l *= f;
-              if (grow) m = top;
-            }
-          } else if (grow) {
-            m = top;
-          }
-          l += tile_terms<E>(sc, soft, here, m == -INFINITY ? 0.f : m);
-          tmem_st_wait();
-        } else if (t > first) {
+          here = min(w.len - t * kTile, kTile);
+          top = tile_max(sc, soft);
+          grow = top > m + kGrow || (m == -INFINITY && top > m);
+        }
+        if (t > first) {
+          // the group's P V before this one: O may be touched
           if (!(ok = warp_wait(ctl, &ctl->pv_done[g], pv_used & 1u, a.err))) break;
           ++pv_used;
+          if (__any_sync(0xffffffffu, grow && r < w.rows)) {
+            // O of the tiles before moves to the new reference
+            tc_fence_after();
+            const float f = grow ? (m == -INFINITY ? 0.f : ex2_approx(m - top)) : 1.f;
+#pragma unroll 1
+            for (int i = 0; i < a.D; i += 32) {
+              uint32_t o[32];
+              tmem_ld32(lanes + kColO + i, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st32(lanes + kColO + i, o);
+            }
+            l *= f;
+            if (grow) m = top;
+          }
+        } else if (grow) {
+          m = top;
+        }
+        if (live) {
+          l += tile_terms<E>(sc, soft, here, m == -INFINITY ? 0.f : m);
+          tmem_st_wait();
         }
         tc_fence_before();
         __syncwarp();
@@ -854,37 +934,35 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       if (!ok) break;
       tile0 += w.t1 - w.t0;
-      if (first < w.t1) {
-        // this group's share of the part's result
-        if (!(ok = warp_wait(ctl, &ctl->pv_done[g], pv_used & 1u, a.err))) break;
-        ++pv_used;
-        tc_fence_after();
-        if (live) {
-          long long at = (static_cast<long long>(blockIdx.x) * kGroups + g) * kTile + r;
-          if (w.first && r < w.rows) {
-            int q, h;
-            w.row(a, r, q, h);
-            at = (static_cast<long long>((w.e < a.P ? 0 : kGroups) + g) * a.B + q) * a.Hq + h;
-          }
-          float* dst = (w.first ? a.o_base : a.o_extra) + at * a.D;
-#pragma unroll 1
-          for (int i = 0; i < a.D; i += 32) {
-            uint32_t o[32];
-            tmem_ld32(lanes + kColO + i, o);
-            tmem_ld_wait();
-            if (r < w.rows) {
-#pragma unroll
-              for (int k = 0; k < 32; k += 4)
-                if (i + k < a.D) st_global_v4(dst + i + k, o[k], o[k + 1], o[k + 2], o[k + 3]);
-            }
-          }
-          if (r < w.rows) (w.first ? a.ml_base : a.ml_extra)[at] = make_float2(m, l);
+      if (first >= w.t1) continue;
+      // this group's share of the part's result
+      if (!warp_wait(ctl, &ctl->pv_done[g], pv_used & 1u, a.err)) break;
+      ++pv_used;
+      tc_fence_after();
+      if (live) {
+        long long at = (static_cast<long long>(blockIdx.x) * kGroups + g) * kTile + r;
+        if (w.first && r < w.rows) {
+          int q, h;
+          part_row(a, w, r, q, h);
+          at = (static_cast<long long>((w.e < a.P ? 0 : kGroups) + g) * a.B + q) * a.Hq + h;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->o_free[g]);
+        float* dst = (w.first ? a.o_base : a.o_extra) + at * a.D;
+#pragma unroll 1
+        for (int i = 0; i < a.D; i += 32) {
+          uint32_t o[32];
+          tmem_ld32(lanes + kColO + i, o);
+          tmem_ld_wait();
+          if (r < w.rows) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              if (i + k < a.D) st_global_v4(dst + i + k, o[k], o[k + 1], o[k + 2], o[k + 3]);
+          }
+        }
+        if (r < w.rows) (w.first ? a.ml_base : a.ml_extra)[at] = make_float2(m, l);
       }
-      w.next();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->o_free[g]);
     }
   }
   __syncwarp();
@@ -1115,16 +1193,46 @@ extern "C" int rz_group_decode_attn(const void* q, const int64_t* q_stride, cons
   m.k = m.v = m.q_own;
   a.paged_tma = n_pages > 0 && page_size % 8 == 0 &&
                 (page_size % kTile == 0 || kTile % page_size == 0);
+  a.fold = kFoldNone;
+  if (a.paged_tma && D == kMaxD && page_size <= 16) {
+    // small pages: both 64-column halves in one box, interleaved by groups of
+    // 8 rows, as each box takes the TMA unit some 58 clocks.  16 x 8 responses
+    // of 1,024 to 8,192 tokens, one box and two: pages of 8 tokens 575 and 822
+    // us, of 16 521 and 573, of 32 517 and 484, of 64 517 and 489
+    const auto folds = [&](const int64_t* s) {
+      if (Hkv == 1 || s[2] == D) return kFoldHeads;
+      return (n_pages == 1 || s[0] == Hkv * s[2]) &&
+                     static_cast<int64_t>(n_pages) * Hkv < (int64_t(1) << 31)
+                 ? kFoldPages
+                 : kFoldNone;
+    };
+    const Fold fk = folds(kv_stride), fv = folds(kv_stride + 3);
+    if (fk == fv) a.fold = fk;
+  }
+  a.group_bytes = a.fold == kFoldNone ? 1024 : 2048;
+  a.half_bytes = a.fold == kFoldNone ? kHalf : 1024;
   if (a.paged_tma) {
-    const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(Hkv),
-                              static_cast<uint64_t>(page_size), static_cast<uint64_t>(n_pages)};
-    const uint32_t box[4] = {64, 1, static_cast<uint32_t>(page_size < kTile ? page_size : kTile),
-                             1};
+    const uint64_t groups = static_cast<uint64_t>(page_size) / 8;
+    const uint32_t box_groups = static_cast<uint32_t>(page_size < kTile ? page_size : kTile) / 8;
+    const uint64_t heads = static_cast<uint64_t>(Hkv), pages = static_cast<uint64_t>(n_pages);
     for (int i = 0; i < 2; ++i) {
-      const int64_t* ks = kv_stride + 3 * i;
-      const uint64_t st[3] = {bytes(ks[2], Hkv), bytes(ks[1], page_size), bytes(ks[0], n_pages)};
-      if ((Hkv > 1 && ks[2] <= 0) || (page_size > 1 && ks[1] <= 0) || (n_pages > 1 && ks[0] <= 0) ||
-          !make_tmap_16bit(i == 0 ? &m.k : &m.v, i == 0 ? k_cache : v_cache, 4, dims, st, box))
+      const int64_t* s = kv_stride + 3 * i;  // page, token, head
+      const uint64_t row = bytes(s[1], page_size), row8 = row * 8;
+      uint64_t dims[5] = {static_cast<uint64_t>(D), 8, heads, groups, pages};
+      uint64_t st[4] = {row, bytes(s[2], Hkv), row8, bytes(s[0], n_pages)};
+      uint32_t box[5] = {64, 8, 1, box_groups, 1};
+      if (a.fold != kFoldNone) {
+        dims[0] = 64;
+        dims[2] = a.fold == kFoldHeads ? heads * 2 : 2;
+        st[1] = 128;
+        box[2] = 2;
+        if (a.fold == kFoldPages) {
+          dims[4] = heads * pages;
+          st[3] = bytes(s[2], 2);
+        }
+      }
+      if ((Hkv > 1 && s[2] <= 0) || (page_size > 1 && s[1] <= 0) || (n_pages > 1 && s[0] <= 0) ||
+          !make_tmap_16bit(i == 0 ? &m.k : &m.v, i == 0 ? k_cache : v_cache, 5, dims, st, box))
         a.paged_tma = 0;  // a stride that no map takes: the copies do
     }
   }

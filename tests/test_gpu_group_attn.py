@@ -129,12 +129,13 @@ def test_matches_the_formula(rz, case):
 
 @pytest.mark.parametrize("layout", ["plain", "heads_first", "side_by_side"])
 @pytest.mark.parametrize("fill", [float("nan"), float("inf")])
-def test_strides_and_what_lies_past_the_lengths(rz, layout, fill):
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 16), (128, 256), (96, 32), (128, 40)])
+def test_strides_and_what_lies_past_the_lengths(rz, layout, fill, D, page):
     """Other cache layouts; NaN or inf in every place that holds no token."""
-    a = _build(BF, 8, 2, 64, 16, [2, 3], [77, 300], [1, 40, 0, 129, 16], seed=5, layout=layout,
+    a = _build(BF, 8, 2, D, page, [2, 3], [77, 300], [1, 40, 0, 129, 16], seed=5, layout=layout,
                fill=fill)
     # queries inside a fused projection's rows
-    wide = torch.empty(5, 12, 64, dtype=BF, device=DEV)
+    wide = torch.empty(5, 12, D, dtype=BF, device=DEV)
     wide[:, 2:10] = a["q"]
     a["q"] = wide[:, 2:10]
     out, lse = rz.rz_group_decode_attn(**a)

@@ -4,11 +4,27 @@
 // What is kept is a head of the row's order (logits descending, ties by the
 // lowest index), so three cuts give three heads and the shortest is kept:
 // every test is "key > t, or key = t and index <= i" with the logit's bits as
-// an ordered 32-bit key.  Top-k's t is found by its count, top-p's by its
-// mass, 8 bits of the key at a time; the masses are the 64-bit integers of
-// rz_fixexp.cuh, whose sums come out the same in every order, so the atomics
+// an ordered 32-bit key.  The masses are the 64-bit integers of rz_fixexp.cuh,
+// whose sums come out the same in every order, so the atomics and exchanges
 // below change nothing from run to run and every decision is that of exact
 // arithmetic.
+//
+// A row is read from memory once: a cluster of up to eight CTAs holds it in
+// shared memory, a slice of whole 2,048-column chunks each, and passes over it
+//   1  while it arrives: its maximum and minimum;
+//   2  (top-k, top-p) counts in 2,048 bins linear in y = (max - z) log2(e) / tau;
+//      from the counts and the bins' edges follow the bin of the k-th logit
+//      and, as bounds on every mass, the few bins that top-p's border can be in;
+//   3  (top-p) the exact masses above and below those bins; (both) what is in
+//      them goes to a list, in which the first CTA finds the border by 8 bits
+//      of the key at a time (a list that overflows: the same over the row);
+//   4  the kept set's bits, the log-sum-exp as the learner takes it, the kept
+//      mass of each chunk; then the chunk and the column where the running sum
+//      passes u.
+// A pass costs 5 to 10 instructions a logit, an exact weight 35.  That bounds
+// a large batch, not the memory: the weight is evaluated once a logit for
+// top-p, and again only for what is kept.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -21,8 +37,16 @@
 namespace rz {
 namespace {
 
-constexpr int kFilterThreads = 1024;
+namespace cg = cooperative_groups;
+
+constexpr int kFilterThreads = 512;
 constexpr int kFilterWarps = kFilterThreads / 32;
+constexpr int kMaxParts = 8;      // CTAs of a row
+constexpr int kBins = 2048;
+constexpr int kOwnList = 512;     // list entries of one CTA
+constexpr int kList = 1024;       // of the row
+constexpr size_t kSliceMax = 81920;  // two CTAs an SM
+constexpr size_t kSmemLimit = 232448;  // of a CTA alone on its SM
 
 __device__ const FixTable g_fix_table = make_fix_table();
 
@@ -38,6 +62,7 @@ struct FilterArgs {
   uint32_t* keep;
   int* err;
   int V, words, chunks, fix_bits;
+  int per;  // chunks of a CTA
 };
 
 // Order of the logits as unsigned integers; -0 counts as +0.
@@ -59,18 +84,6 @@ struct Cut {
     return k > t || (k == t && v <= last);
   }
 };
-struct CutKept {
-  Cut cut;
-  int V;
-  __device__ __forceinline__ uint32_t before(int) const { return 0xffu; }
-  __device__ __forceinline__ uint32_t after(int col, const float (&v)[8], uint32_t) const {
-    uint32_t bits = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (col + i < V && cut.has(v[i], col + i)) bits |= 1u << i;
-    return bits;
-  }
-};
 
 // x * (f * 2^64) / 2^64, floor, for a float 0 <= f < 1; *exact = no remainder.
 __device__ __forceinline__ uint64_t mul_frac(uint64_t x, float f, bool* exact) {
@@ -78,297 +91,824 @@ __device__ __forceinline__ uint64_t mul_frac(uint64_t x, float f, bool* exact) {
   *exact = x * m == 0;
   return __umul64hi(x, m);
 }
+// Smallest integer >= p * x, at least 1: a token is in while the mass above it
+// is less than this.
+__device__ __forceinline__ uint64_t mass_target(uint64_t x, float p) {
+  bool exact = true;
+  uint64_t t = p > 0.f ? mul_frac(x, p, &exact) : 0;
+  if (!exact || t == 0) ++t;
+  return t;
+}
+
+struct Entry {
+  uint32_t key;
+  int idx;
+};
 
 struct FilterShared {
   uint64_t table[kFixTable];
-  uint32_t count[256], lo[256], hi[256];
+  union {
+    uint32_t bins[kBins];
+    Entry list[kList];  // (first CTA) once the bins have been read
+  };
+  union {
+    Entry own[kOwnList];
+    struct {
+      uint32_t count[256], lo[256], hi[256];
+    } digit;
+  };
   uint64_t red[kFilterWarps];
-  float redf[kFilterWarps];
-  uint32_t digit;
-  uint64_t above;  // count or mass above the digit
-  uint64_t target;
-  FixScale scale;
-  int bad, last, n, warp;
+  float redf[2 * kFilterWarps];
+  // written by every CTA of the cluster
+  float part_max[kMaxParts], part_min[kMaxParts];
+  int part_nan[kMaxParts], part_list[kMaxParts], part_n[kMaxParts];
+  uint64_t part_a[kMaxParts], part_b[kMaxParts];
+  // written by the first CTA
+  int bin_k, bin_lo, bin_hi;
+  uint32_t above_k;
+  uint32_t cut_t;
+  int cut_last;
+  uint32_t digit_now;
+  uint64_t above;
+  // scratch
+  int own_n, hit;
   uint64_t rest;
 };
 
-__device__ __forceinline__ uint64_t block_sum(FilterShared& s, uint64_t x) {
+template <class Tv>
+__device__ __forceinline__ Tv warp_sum(Tv x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ uint64_t block_sum(FilterShared& s, uint64_t x) {
+  x = warp_sum(x);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5] = x;
   __syncthreads();
   uint64_t t = 0;
+#pragma unroll
   for (int w = 0; w < kFilterWarps; ++w) t += s.red[w];
   return t;
 }
+// Exclusive sum over the block's threads, and the total.
+template <class Tv>
+__device__ __forceinline__ Tv block_scan(Tv* scratch, Tv x, Tv& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Tv inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Tv y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  __syncthreads();
+  if (lane == 31) scratch[warp] = inc;
+  __syncthreads();
+  Tv base = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kFilterWarps; ++w) {
+    const Tv v = scratch[w];
+    if (w < warp) base += v;
+    total += v;
+  }
+  return base + inc - x;
+}
 
-// The largest key t with (count or mass of the keys >= t) >= target, and what
-// lies above t.  Only elements with key >= floor take part.
-template <class E, bool kMass>
-__device__ void select(FilterShared& s, const E* z, int V, uint32_t floor, uint64_t target,
-                       uint32_t& t_out, uint64_t& above_out) {
+// ------------------------------------------------------------------ selection
+// The largest key t such that the keys >= t have a count (or mass) of at least
+// `target`, and what lies above it, 8 bits at a time.  What is looked through:
+// the row's logits (every CTA takes part) or the list (the first CTA).
+enum Measure { kCount, kMass, kIndex };  // kIndex: count, of the keys ~index
+
+__device__ __forceinline__ void digit_add(FilterShared& s, uint32_t b, uint64_t w, bool mass) {
+  if (mass) {
+    const uint32_t wl = static_cast<uint32_t>(w);
+    const uint32_t old = atomicAdd(&s.digit.lo[b], wl);
+    atomicAdd(&s.digit.hi[b], static_cast<uint32_t>(w >> 32) + (old + wl < old ? 1u : 0u));
+  } else {
+    atomicAdd(&s.digit.count[b], static_cast<uint32_t>(w));
+  }
+}
+
+// Warp 0 of the first CTA: the digit where the target is reached, given each
+// digit's amount.
+template <class Amount>
+__device__ __forceinline__ void digit_find(FilterShared& s, uint64_t target, uint64_t above,
+                                           const Amount& amount) {
+  const int lane = threadIdx.x & 31;
+  uint64_t x[8], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = amount(255 - 8 * lane - i);  // lane 0 has the largest digits
+    sum += x[i];
+  }
+  uint64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  const uint32_t reached = __ballot_sync(0xffffffffu, above + inc >= target);
+  const int who = reached ? __ffs(reached) - 1 : 31;
+  if (lane == who) {
+    uint64_t a = above + inc - sum;
+    int i = 0;
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+      if (i == k && a + x[k] < target) {
+        a += x[k];
+        i = k + 1;
+      }
+    s.digit_now = 255 - 8 * lane - i;
+    s.above = a;
+  }
+}
+
+// Over the list of n entries, first CTA only.  floor: smaller keys are left out;
+// equal: (kIndex) only entries of this key.
+__device__ void select_list(FilterShared& s, const FixScale& scale, Measure what, int n,
+                            uint32_t floor, uint32_t equal, uint64_t target, uint32_t& t_out,
+                            uint64_t& above_out) {
   uint32_t prefix = 0;
   uint64_t above = 0;
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kFilterThreads) s.count[i] = s.lo[i] = s.hi[i] = 0;
+    for (int i = threadIdx.x; i < 256; i += kFilterThreads)
+      s.digit.count[i] = s.digit.lo[i] = s.digit.hi[i] = 0;
     __syncthreads();
-    for (int v = threadIdx.x; v < V; v += kFilterThreads) {
-      const float x = to_f32(z[v]);
-      const uint32_t k = order_key(x);
-      if (k < floor || (shift < 24 && (k >> (shift + 8)) != prefix)) continue;
-      const uint32_t b = (k >> shift) & 255u;
-      if (kMass) {
-        const uint64_t w = fix_weight(s.scale, s.table, x);
-        const uint32_t wl = static_cast<uint32_t>(w);
-        const uint32_t old = atomicAdd(&s.lo[b], wl);
-        atomicAdd(&s.hi[b], static_cast<uint32_t>(w >> 32) + (old + wl < old ? 1u : 0u));
-      } else {
-        atomicAdd(&s.count[b], 1u);
-      }
+    for (int i = threadIdx.x; i < n; i += kFilterThreads) {
+      const Entry e = s.list[i];
+      const uint32_t k = what == kIndex ? ~static_cast<uint32_t>(e.idx) : e.key;
+      if (what == kIndex ? e.key != equal : e.key < floor) continue;
+      if (shift < 24 && (k >> (shift + 8)) != prefix) continue;
+      digit_add(s, (k >> shift) & 255u,
+                what == kMass ? fix_weight(scale, s.table, key_value(e.key)) : 1, what == kMass);
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-      uint64_t a = above;
-      int b = 255;
-      for (; b > 0; --b) {
-        const uint64_t x = kMass ? (static_cast<uint64_t>(s.hi[b]) << 32) + s.lo[b]
-                                 : static_cast<uint64_t>(s.count[b]);
-        if (a + x >= target) break;
-        a += x;
-      }
-      s.digit = b;
-      s.above = a;
-    }
+    if (threadIdx.x < 32)
+      digit_find(s, target, above, [&](int b) {
+        return what == kMass ? (static_cast<uint64_t>(s.digit.hi[b]) << 32) + s.digit.lo[b]
+                             : static_cast<uint64_t>(s.digit.count[b]);
+      });
     __syncthreads();
-    prefix = prefix << 8 | s.digit;
+    prefix = prefix << 8 | s.digit_now;
     above = s.above;
+  }
+  __syncthreads();
+  t_out = prefix;
+  above_out = above;
+}
+
+// Over the row: every CTA of the cluster looks through its slice z (columns
+// v0 .. v0 + n - 1), the first one adds up.
+template <class E>
+__device__ void select_row(FilterShared& s, cg::cluster_group& cluster, const FixScale& scale,
+                           Measure what, const E* z, int v0, int n, uint32_t floor, uint32_t equal,
+                           uint64_t target, uint32_t& t_out, uint64_t& above_out) {
+  const int parts = static_cast<int>(cluster.num_blocks());
+  uint32_t prefix = 0;
+  uint64_t above = 0;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = threadIdx.x; i < 256; i += kFilterThreads)
+      s.digit.count[i] = s.digit.lo[i] = s.digit.hi[i] = 0;
     __syncthreads();
+    for (int i0 = 0; i0 < n; i0 += kFilterThreads) {
+      const int i = i0 + threadIdx.x;
+      bool in = false;
+      uint32_t k = 0, key = 0;
+      if (i < n) {
+        key = order_key(to_f32(z[i]));
+        k = what == kIndex ? ~static_cast<uint32_t>(v0 + i) : key;
+        in = what == kIndex ? key == equal : key >= floor;
+        in = in && (shift == 24 || (k >> (shift + 8)) == prefix);
+      }
+      const uint32_t who = __ballot_sync(0xffffffffu, in);
+      if (who == 0) continue;
+      // a row of equal logits would put every lane on one counter
+      const uint32_t b = (k >> shift) & 255u;
+      const int first = __ffs(who) - 1;
+      const uint32_t key0 = __shfl_sync(0xffffffffu, key, first);
+      const uint32_t b0 = __shfl_sync(0xffffffffu, b, first);
+      if (__all_sync(0xffffffffu, !in || (key == key0 && b == b0))) {
+        if (static_cast<int>(threadIdx.x & 31) == first) {
+          const uint64_t c = __popc(who);
+          digit_add(s, b, what == kMass ? c * fix_weight(scale, s.table, key_value(key)) : c,
+                    what == kMass);
+        }
+      } else if (in) {
+        digit_add(s, b, what == kMass ? fix_weight(scale, s.table, key_value(key)) : 1,
+                  what == kMass);
+      }
+    }
+    cluster.sync();
+    if (cluster.block_rank() == 0) {
+      if (threadIdx.x < 32)
+        digit_find(s, target, above, [&](int b) {
+          uint64_t x = 0;
+          for (int r = 0; r < parts; ++r) {
+            const FilterShared* o = cluster.map_shared_rank(&s, r);
+            x += what == kMass ? (static_cast<uint64_t>(o->digit.hi[b]) << 32) + o->digit.lo[b]
+                               : static_cast<uint64_t>(o->digit.count[b]);
+          }
+          return x;
+        });
+      __syncthreads();
+      if (threadIdx.x < static_cast<unsigned>(parts)) {
+        FilterShared* o = cluster.map_shared_rank(&s, threadIdx.x);
+        if (threadIdx.x != 0) {
+          o->digit_now = s.digit_now;
+          o->above = s.above;
+        }
+      }
+    }
+    cluster.sync();
+    prefix = prefix << 8 | s.digit_now;
+    above = s.above;
   }
   t_out = prefix;
   above_out = above;
 }
 
-template <class E>
-__global__ void __launch_bounds__(kFilterThreads) filter_sample_kernel(const FilterArgs a) {
+// ------------------------------------------------------------------ bins
+// y of a logit as the weights take it (rounded: bins only need an order that
+// agrees with the logits'), and its bin.
+struct Binning {
+  float zmax, c_hi, scale;
+  __device__ __forceinline__ int bin(float z) const {
+    const float y = __fmul_rn(__fsub_rn(zmax, z), c_hi);
+    return static_cast<int>(fminf(__fmul_rn(y, scale), static_cast<float>(kBins - 1)));
+  }
+  // Bounds on the weight of what is in bin b: the table's steps of 2^-11 just
+  // outside of it (and one more for the roundings of y).
+  __device__ __forceinline__ uint64_t most(const uint64_t* tab, int drop, int b) const {
+    const int k = static_cast<int>(floorf(b / scale * kFixTable)) - 2;
+    return at(tab, drop, k < 0 ? 0 : k) + 1;
+  }
+  __device__ __forceinline__ uint64_t least(const uint64_t* tab, int drop, int b) const {
+    if (b == kBins - 1) return 0;
+    return at(tab, drop, static_cast<int>(ceilf((b + 1) / scale * kFixTable)) + 2);
+  }
+  static __device__ __forceinline__ uint64_t at(const uint64_t* tab, int drop, int k) {
+    const int sh = (k >> kFixTableBits) + drop;
+    return sh > 60 ? 0 : (tab[k & (kFixTable - 1)] >> sh) >> 1;
+  }
+};
+
+template <class E, bool kResident>
+__global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
+    filter_sample_kernel(const FilterArgs a) {
   extern __shared__ uint8_t smem[];
   FilterShared& s = *reinterpret_cast<FilterShared*>(smem);
   float2* states = reinterpret_cast<float2*>(smem + (sizeof(FilterShared) + 15) / 16 * 16);
-  const long long row = blockIdx.x;
-  const E* z = static_cast<const E*>(a.logits) + row * a.ld;
+  uint64_t* chunk_mass = reinterpret_cast<uint64_t*>(states + a.chunks);  // own chunks
+  E* slice = reinterpret_cast<E*>(smem + ((sizeof(FilterShared) + 15) / 16 * 16 +
+                                          (a.chunks + a.per) * 8 + 127) / 128 * 128);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int parts = static_cast<int>(cluster.num_blocks());
+  const int part = static_cast<int>(cluster.block_rank());
+  const bool lead = part == 0;
+  const long long row = blockIdx.x / parts;
+  const E* zrow = static_cast<const E*>(a.logits) + row * a.ld;
   const int V = a.V;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t* keep = a.keep ? a.keep + row * a.words : nullptr;
+  const int v0 = min(part * a.per * kKeepChunk, V);
+  const int n = min(V - v0, a.per * kKeepChunk);  // columns of this CTA
+  const E* z = kResident ? slice : zrow + v0;
 
-  // ---- the row's maximum, NaN and +inf
-  float m = -INFINITY;
+  // ---- 1: the slice, its maximum, minimum and NaNs
+  float mx = -INFINITY, mn = INFINITY;
   bool nan = false;
-  int finite = 0;
-  for (int v = threadIdx.x; v < V; v += kFilterThreads) {
-    const float x = to_f32(z[v]);
+  const auto look = [&](float x) {
     nan |= !(x == x);
-    finite += x > -INFINITY;
-    m = fmaxf(m, x);
+    mx = fmaxf(mx, x);
+    mn = fminf(mn, x > -INFINITY ? x : mn);
+  };
+  for (int i = threadIdx.x; i < kFixTable; i += kFilterThreads) s.table[i] = g_fix_table.v[i];
+  for (int i = threadIdx.x; i < kBins; i += kFilterThreads) s.bins[i] = 0;
+  if (threadIdx.x == 0) s.own_n = 0;
+  {
+    const E* src = zrow + v0;
+    constexpr int kPer = 16 / sizeof(E);
+    const int vecs = row_aligned(src) ? n / kPer : 0;
+    const uint4* src4 = reinterpret_cast<const uint4*>(src);
+    uint4* dst4 = reinterpret_cast<uint4*>(slice);
+    for (int i0 = threadIdx.x; i0 < vecs; i0 += 4 * kFilterThreads) {
+      uint4 q[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i0 + u * kFilterThreads < vecs) q[u] = src4[i0 + u * kFilterThreads];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * kFilterThreads;
+        if (i < vecs) {
+          if (kResident) dst4[i] = q[u];
+          const E* e = reinterpret_cast<const E*>(&q[u]);
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) look(to_f32(e[k]));
+        }
+      }
+    }
+    for (int i = vecs * kPer + threadIdx.x; i < n; i += kFilterThreads) {
+      const E e = src[i];
+      if (kResident) slice[i] = e;
+      look(to_f32(e));
+    }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) s.redf[warp] = m;
-  for (int i = threadIdx.x; i < kFixTable; i += kFilterThreads) s.table[i] = g_fix_table.v[i];
-  const bool any_nan = __syncthreads_or(nan);
-  const int n_finite = static_cast<int>(block_sum(s, finite));
-  m = s.redf[0];
-  for (int w = 1; w < kFilterWarps; ++w) m = fmaxf(m, s.redf[w]);
+  for (int o = 16; o > 0; o >>= 1) {
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+  }
+  if (lane == 0) {
+    s.redf[warp] = mx;
+    s.redf[kFilterWarps + warp] = mn;
+  }
+  const int any_nan = __syncthreads_or(nan);
+  if (parts > 1) cluster.sync();  // every CTA runs before its memory is written
+  if (threadIdx.x < static_cast<unsigned>(parts)) {
+    mx = s.redf[0];
+    mn = s.redf[kFilterWarps];
+    for (int w = 1; w < kFilterWarps; ++w) {
+      mx = fmaxf(mx, s.redf[w]);
+      mn = fminf(mn, s.redf[kFilterWarps + w]);
+    }
+    FilterShared* o = cluster.map_shared_rank(&s, threadIdx.x);
+    o->part_max[part] = mx;
+    o->part_min[part] = mn;
+    o->part_nan[part] = any_nan;
+  }
+  cluster.sync();
+  float zmax = s.part_max[0], zmin = s.part_min[0];
+  int bad_logits = s.part_nan[0];
+  for (int i = 1; i < parts; ++i) {
+    zmax = fmaxf(zmax, s.part_max[i]);
+    zmin = fminf(zmin, s.part_min[i]);
+    bad_logits |= s.part_nan[i];
+  }
 
-  float temperature = a.temperature ? a.temperature[row] : 1.f;
-  const bool greedy = temperature == 0.f;
+  const float temperature = a.temperature ? a.temperature[row] : 1.f;
   const float tau = row_tau(a.temperature, row);
   const float u = a.uniform[row];
   const float p = a.top_p ? a.top_p[row] : 1.f;
   const float mp = a.min_p ? a.min_p[row] : 0.f;
   int k = a.top_k ? a.top_k[row] : 0;
-  if (k <= 0 || k > n_finite) k = n_finite;
-  if (greedy) k = 1;
+  if (k <= 0 || k > V) k = V;
+  if (temperature == 0.f) k = 1;
   const bool bad_param = !(tau == tau) || !(u >= 0.f && u < 1.f) || !(p == p) || !(mp <= 1.f);
-  const bool bad_row = any_nan || !(m < INFINITY) || n_finite == 0;
-  if (bad_param || bad_row) {
-    if (keep)
-      for (int i = threadIdx.x; i < a.words; i += kFilterThreads) keep[i] = 0u;
-    if (threadIdx.x == 0) {
+  bad_logits |= !(zmax < INFINITY && zmax > -INFINITY);
+  if (bad_param || bad_logits) {
+    if (a.keep)
+      for (int i = threadIdx.x; i < (n + 31) / 32; i += kFilterThreads)
+        a.keep[row * a.words + v0 / 32 + i] = 0u;
+    if (lead && threadIdx.x == 0) {
       a.tokens[row] = -1;
       a.logprob[row] = __int_as_float(0x7fc00000);
       if (a.kept) a.kept[row] = 0;
       if (a.err)
-        atomicOr(a.err, (bad_param ? RZ_DEVERR_PARAM : 0) | (bad_row ? RZ_DEVERR_LOGITS : 0));
+        atomicOr(a.err, (bad_param ? RZ_DEVERR_PARAM : 0) | (bad_logits ? RZ_DEVERR_LOGITS : 0));
     }
-    return;
+    return;  // the whole cluster does; nobody's memory is in use
   }
-  if (threadIdx.x == 0) {
+  FixScale scale;
+  {
     const double c = 1.44269504088896340736 / static_cast<double>(tau);
-    s.scale.zmax = m;
-    s.scale.c_hi = static_cast<float>(c);
-    s.scale.c_lo = static_cast<float>(c - static_cast<double>(s.scale.c_hi));
-    s.scale.drop = kFixQ - a.fix_bits;
+    scale.zmax = zmax;
+    scale.c_hi = static_cast<float>(c);
+    scale.c_lo = static_cast<float>(c - static_cast<double>(scale.c_hi));
+    scale.drop = kFixQ - a.fix_bits;
   }
-  __syncthreads();
-  const FixScale scale = s.scale;
 
-  // ---- the cuts: key > t, or one of the first `ties` at key = t
-  uint32_t t = kKeyNegInf;
+  // ---- 2, 3: the cut
+  uint32_t t = kKeyNegInf;  // key > t, or one of the first `ties` at key = t
   long long ties = 0;
-  if (k < n_finite) {
-    uint64_t above;
-    select<E, false>(s, z, V, 0u, k, t, above);
-    ties = k - static_cast<long long>(above);
-  }
-  if (p < 1.f) {
-    uint64_t total = 0;
-    for (int v = threadIdx.x; v < V; v += kFilterThreads) {
-      const float x = to_f32(z[v]);
-      if (order_key(x) > t) total += fix_weight(scale, s.table, x);
-    }
-    total = block_sum(s, total);
-    if (ties > 0) total += ties * fix_weight(scale, s.table, key_value(t));
-    bool exact = true;
-    uint64_t target = p > 0.f ? mul_frac(total, p, &exact) : 0;
-    if (!exact || target == 0) ++target;  // a token is in while what lies above it < p * total
-    uint32_t tp;
-    uint64_t above;
-    select<E, true>(s, z, V, ties > 0 ? t : t + 1, target, tp, above);
-    const uint64_t w = fix_weight(scale, s.table, key_value(tp));
-    long long n = w > 0 ? static_cast<long long>((target - above + w - 1) / w) : 1;
-    if (tp == t && n > ties) n = ties;
-    t = tp;
-    ties = n;
-  }
-  if (mp > 0.f) {
-    const float zmin = __double2float_ru(static_cast<double>(m) +
-                                         static_cast<double>(tau) * log(static_cast<double>(mp)));
-    const uint32_t km = order_key(zmin);
-    if (km > t) {
-      t = km - 1;
-      ties = 0;
-    }
-  }
-
-  // ---- the index of the last tie that is in
-  const int seg = (V + 32 * kFilterWarps - 1) / (32 * kFilterWarps) * 32;
-  const int v0 = warp * seg, v1 = min(V, v0 + seg);
   int last = -1;
-  if (ties > 0) {
-    int n = 0;
-    for (int v = v0 + lane; v < v1; v += 32) n += order_key(to_f32(z[v])) == t;
+  const bool want_k = k < V, want_p = p < 1.f;
+  if (want_k || want_p) {
+    Binning bn;
+    bn.zmax = zmax;
+    bn.c_hi = scale.c_hi;
+    {
+      // 2,048 bins over the row's range, at most 32 (in y; what is beyond
+      // weighs nothing) and no finer than the table
+      const float range = __fmul_rn(__fsub_rn(zmax, zmin), scale.c_hi);
+      bn.scale = (kBins - 2) / fminf(fmaxf(range, 1.f), 32.f);
+    }
+    for (int i = threadIdx.x; i < n; i += kFilterThreads) {
+      const float x = to_f32(z[i]);
+      if (x > -INFINITY) atomicAdd(&s.bins[bn.bin(x)], 1u);
+    }
+    __syncthreads();
+    if (parts > 1) {
+      if (!lead) {
+        FilterShared* o = cluster.map_shared_rank(&s, 0);
+        for (int i = threadIdx.x; i < kBins; i += kFilterThreads)
+          if (s.bins[i]) atomicAdd(&o->bins[i], s.bins[i]);
+      }
+      cluster.sync();
+    }
+    if (lead) {
+      constexpr int kEach = kBins / kFilterThreads;
+      const int b0 = threadIdx.x * kEach;
+      if (threadIdx.x == 0) {
+        s.bin_k = kBins;  // no cut by count
+        s.above_k = 0;
+        s.bin_lo = kBins;
+        s.bin_hi = -1;
+      }
+      uint32_t c[kEach], sum = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    __syncthreads();
-    if (lane == 0) s.red[warp] = n;
-    if (threadIdx.x == 0) s.last = V - 1;
-    __syncthreads();
-    long long before = 0;
-    for (int w = 0; w < warp; ++w) before += static_cast<long long>(s.red[w]);
-    if (before < ties && before + n >= ties) {
-      long long left = ties - before;  // the left-th tie of this warp's columns
-      for (int v = v0; v < v1; v += 32) {
-        const bool tie = v + lane < v1 && order_key(to_f32(z[v + lane])) == t;
-        const uint32_t b = __ballot_sync(0xffffffffu, tie);
-        if (left <= __popc(b)) {
-          if (lane == 0) s.last = v + static_cast<int>(__fns(b, 0, static_cast<int>(left)));
-          break;
+      for (int i = 0; i < kEach; ++i) sum += c[i] = s.bins[b0 + i];
+      uint32_t all;
+      uint32_t before = block_scan(reinterpret_cast<uint32_t*>(s.red), sum, all);
+      if (want_k && all > static_cast<uint32_t>(k)) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          if (before < static_cast<uint32_t>(k) && before + c[i] >= static_cast<uint32_t>(k)) {
+            s.bin_k = b0 + i;
+            s.above_k = before;
+          }
+          before += c[i];
         }
-        left -= __popc(b);
+      }
+      __syncthreads();
+      if (want_p) {
+        // bounds on the masses of the bins, in top-k's head
+        const int bin_k = s.bin_k;
+        uint64_t lo[kEach], hi[kEach], lo_sum = 0, hi_sum = 0, lo_all, hi_all;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const int b = b0 + i;
+          const uint32_t m = b < bin_k ? c[i] : (b == bin_k ? k - s.above_k : 0u);
+          c[i] = m;
+          lo[i] = m ? m * bn.least(s.table, scale.drop, b) : 0;
+          hi[i] = m ? m * bn.most(s.table, scale.drop, b) : 0;
+          lo_sum += lo[i];
+          hi_sum += hi[i];
+        }
+        uint64_t lo_at = block_scan(s.red, lo_sum, lo_all);
+        uint64_t hi_at = block_scan(s.red, hi_sum, hi_all);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          if (c[i]) {
+            // may what lies above be short of p of all, and may what lies
+            // above and here reach it?
+            const uint64_t lo_end = lo_at + lo[i], hi_end = hi_at + hi[i];
+            if (lo_at < mass_target(lo_at + (hi_all - hi_at), p) &&
+                hi_end >= mass_target(hi_end + (lo_all - lo_end), p)) {
+              atomicMin(&s.bin_lo, b0 + i);
+              atomicMax(&s.bin_hi, b0 + i);
+            }
+          }
+          lo_at += lo[i];
+          hi_at += hi[i];
+        }
+      }
+      __syncthreads();
+      if (threadIdx.x > 0 && threadIdx.x < static_cast<unsigned>(parts)) {
+        FilterShared* o = cluster.map_shared_rank(&s, threadIdx.x);
+        o->bin_k = s.bin_k;
+        o->above_k = s.above_k;
+        o->bin_lo = s.bin_lo;
+        o->bin_hi = s.bin_hi;
       }
     }
-    __syncthreads();
-    last = s.last;
+    if (parts > 1) cluster.sync();
+    const int bin_k = s.bin_k, bin_lo = s.bin_lo, bin_hi = s.bin_hi;
+    const bool cut_k = bin_k < kBins;
+    // the exact masses above the band, and of all of top-k's head but the
+    // band and bin_k; what is in these two is listed
+    uint64_t sum_a = 0, sum_r = 0;
+    for (int i = threadIdx.x; i < n; i += kFilterThreads) {
+      const float x = to_f32(z[i]);
+      const int b = bn.bin(x);
+      if (b > bin_k || !(x > -INFINITY)) continue;
+      if ((want_p && b >= bin_lo && b <= bin_hi) || b == bin_k) {
+        const int at = atomicAdd(&s.own_n, 1);
+        if (at < kOwnList) {
+          s.own[at].key = order_key(x);
+          s.own[at].idx = v0 + i;
+        }
+      } else if (want_p) {
+        const uint64_t w = fix_weight(scale, s.table, x);
+        if (b < bin_lo) sum_a += w;
+        else sum_r += w;
+      }
+    }
+    if (want_p) {
+      sum_a = block_sum(s, sum_a);
+      sum_r = block_sum(s, sum_r);
+    } else {
+      __syncthreads();
+    }
+    const int own = s.own_n;
+    if (threadIdx.x < static_cast<unsigned>(parts)) {
+      FilterShared* o = cluster.map_shared_rank(&s, threadIdx.x);
+      o->part_a[part] = sum_a;
+      o->part_b[part] = sum_r;
+      o->part_list[part] = own;
+    }
+    cluster.sync();
+    int listed = 0, offset = 0;
+    bool fits = true;
+    for (int i = 0; i < parts; ++i) {
+      if (i < part) offset += s.part_list[i];
+      fits = fits && s.part_list[i] <= kOwnList;
+      listed += s.part_list[i];
+    }
+    fits = fits && listed <= kList;
+    if (fits) {
+      Entry* list = cluster.map_shared_rank(&s, 0)->list;
+      for (int i = threadIdx.x; i < own; i += kFilterThreads) list[offset + i] = s.own[i];
+      cluster.sync();
+      if (lead) {
+        uint64_t above;
+        if (cut_k) {
+          // (entries of the band above bin_k are above every key of bin_k)
+          uint32_t tk;
+          uint64_t extra = 0;  // listed entries in bins above bin_k
+          {
+            int c = 0;
+            for (int i = threadIdx.x; i < listed; i += kFilterThreads)
+              c += bn.bin(key_value(s.list[i].key)) < bin_k;
+            extra = block_sum(s, c);
+          }
+          select_list(s, scale, kCount, listed, 0u, 0u, k - s.above_k + extra, tk, above);
+          t = tk;
+          ties = static_cast<long long>(k - s.above_k + extra - above);
+        }
+        if (want_p) {
+          uint64_t base = 0, total = 0;
+          for (int i = 0; i < parts; ++i) {
+            base += s.part_a[i];
+            total += s.part_a[i] + s.part_b[i];
+          }
+          // the listed part of top-k's head
+          uint64_t x = 0;
+          for (int i = threadIdx.x; i < listed; i += kFilterThreads) {
+            const uint32_t key = s.list[i].key;
+            if (key > t) x += fix_weight(scale, s.table, key_value(key));
+          }
+          total += block_sum(s, x);
+          if (ties > 0) total += ties * fix_weight(scale, s.table, key_value(t));
+          const uint64_t target = mass_target(total, p);
+          uint32_t tp;
+          select_list(s, scale, kMass, listed, ties > 0 ? t : t + 1, 0u, target - base, tp, above);
+          const uint64_t w = fix_weight(scale, s.table, key_value(tp));
+          long long m = w > 0 ? static_cast<long long>((target - base - above + w - 1) / w) : 1;
+          if (tp == t && m > ties) m = ties;
+          t = tp;
+          ties = m;
+        }
+        if (ties > 0) {
+          uint32_t at;
+          select_list(s, scale, kIndex, listed, 0u, t, ties, at, above);
+          last = static_cast<int>(~at);
+        }
+        if (threadIdx.x < static_cast<unsigned>(parts)) {
+          FilterShared* o = cluster.map_shared_rank(&s, threadIdx.x);
+          o->cut_t = t;
+          o->cut_last = last;
+        }
+      }
+      cluster.sync();
+      t = s.cut_t;
+      last = s.cut_last;
+    } else {
+      // more in the bins than the list holds: the same over the row
+      uint64_t above;
+      if (cut_k) {
+        select_row(s, cluster, scale, kCount, z, v0, n, 0u, 0u, k, t, above);
+        ties = k - static_cast<long long>(above);
+      }
+      if (want_p) {
+        uint64_t x = 0;
+        for (int i = threadIdx.x; i < n; i += kFilterThreads) {
+          const float y = to_f32(z[i]);
+          if (order_key(y) > t) x += fix_weight(scale, s.table, y);
+        }
+        x = block_sum(s, x);
+        if (threadIdx.x < static_cast<unsigned>(parts))
+          cluster.map_shared_rank(&s, threadIdx.x)->part_a[part] = x;
+        cluster.sync();
+        uint64_t total = 0;
+        for (int i = 0; i < parts; ++i) total += s.part_a[i];
+        if (ties > 0) total += ties * fix_weight(scale, s.table, key_value(t));
+        const uint64_t target = mass_target(total, p);
+        uint32_t tp;
+        select_row(s, cluster, scale, kMass, z, v0, n, ties > 0 ? t : t + 1, 0u, target, tp, above);
+        const uint64_t w = fix_weight(scale, s.table, key_value(tp));
+        long long m = w > 0 ? static_cast<long long>((target - above + w - 1) / w) : 1;
+        if (tp == t && m > ties) m = ties;
+        t = tp;
+        ties = m;
+      }
+      if (ties > 0) {
+        uint32_t at;
+        select_row(s, cluster, scale, kIndex, z, v0, n, 0u, t, ties, at, above);
+        last = static_cast<int>(~at);
+      }
+    }
+  }
+  if (mp > 0.f) {
+    const float zlow = __double2float_ru(static_cast<double>(zmax) +
+                                         static_cast<double>(tau) * log(static_cast<double>(mp)));
+    const uint32_t km = order_key(zlow);
+    if (km > t) {
+      t = km - 1;
+      last = -1;
+    }
   }
   const Cut cut{t, last};
 
-  // ---- kept mass of each warp's columns, the kept set's bits
-  uint64_t mass = 0;
-  int n = 0;
-  for (int v = v0; v < v1; v += 32) {
-    bool in = false;
-    if (v + lane < v1) {
-      const float x = to_f32(z[v + lane]);
-      in = cut.has(x, v + lane);
-      if (in) mass += fix_weight(scale, s.table, x);
-    }
-    const uint32_t b = __ballot_sync(0xffffffffu, in);
-    n += __popc(b);
-    if (keep && lane == 0) keep[v >> 5] = b;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    s.n = 0;
-    s.rest = 0;
-    s.warp = kFilterWarps;
-  }
-  if (lane == 0) s.red[warp] = mass;
-  __syncthreads();
-  // u = 0 is the first kept token whatever its weight rounds to
-  const bool first = u == 0.f;
-  if (lane == 0 && n) {
-    atomicAdd(&s.n, n);
-    if (first) atomicMin(&s.warp, warp);
-  }
-  if (threadIdx.x == 0 && !first) {
-    uint64_t total = 0;
-    for (int w = 0; w < kFilterWarps; ++w) total += s.red[w];
-    bool exact;
-    uint64_t r = mul_frac(total, u, &exact);  // the token: running sum > u * total
-    int w = 0;
-    while (w < kFilterWarps - 1 && r >= s.red[w]) r -= s.red[w++];
-    s.warp = w;
-    s.rest = r;
-  }
-  // ---- log-sum-exp over the kept columns, as the learner takes it
+  // ---- 4: kept bits, log-sum-exp and mass of each chunk (the two passes of
+  // keep_fold, a warp a chunk, with its operations in its order)
   const float c = keep_scale(tau);
-  const bool vec = row_aligned(z);
-  const CutKept kept{cut, V};
-  for (int ch = warp; ch < a.chunks; ch += kFilterWarps) {
-    const float2 st = keep_fold(z, vec, V, ch, c, kept);
-    if (lane == 0) states[ch] = st;
+  const bool vec = kResident || row_aligned(z);
+  const bool first = u == 0.f;  // the first kept token, whatever its weight rounds to
+  uint8_t* keep = a.keep ? reinterpret_cast<uint8_t*>(a.keep + row * a.words) : nullptr;
+  int count = 0;
+  const int own_chunks = (n + kKeepChunk - 1) / kKeepChunk;
+  uint64_t mass_all = 0;
+  for (int ch = warp; ch < own_chunks; ch += kFilterWarps) {
+    uint32_t bits[2] = {0u, 0u};
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = ch * kKeepChunk + 256 * j + 8 * lane;
+      if (i < n) {
+        float v[8];
+        load8(z, vec, n, i, v);
+        uint32_t b = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          if (i + q < n && cut.has(v[q], v0 + i + q)) {
+            b |= 1u << q;
+            m = fmaxf(m, v[q]);
+          }
+        }
+        bits[j >> 2] |= b << (8 * (j & 3));
+        if (keep) keep[(v0 + i) >> 3] = static_cast<uint8_t>(b);
+      }
+    }
+    count += __popc(bits[0]) + __popc(bits[1]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float2 st = make_float2(-INFINITY, 0.f);
+    uint64_t mass = 0;
+    if (m > -INFINITY) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      int top = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t b = (bits[j >> 2] >> (8 * (j & 3))) & 255u;
+        if (b) {
+          float v[8];
+          load8(z, vec, n, ch * kKeepChunk + 256 * j + 8 * lane, v);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            if (!((b >> q) & 1u)) continue;
+            const float e = ex2_approx(__fmul_rn(__fsub_rn(v[q], m), c));
+            const bool is_top = v[q] == m;
+            acc[q & 3] = __fadd_rn(acc[q & 3], is_top ? 0.f : e);
+            top += is_top;
+            mass += first ? 1 : fix_weight(scale, s.table, v[q]);
+          }
+        }
+      }
+      float r = __fadd_rn(__fadd_rn(acc[0], acc[1]), __fadd_rn(acc[2], acc[3]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, o));
+        top += __shfl_xor_sync(0xffffffffu, top, o);
+      }
+      st = make_float2(m, __fadd_rn(r, static_cast<float>(top - 1)));
+      mass = warp_sum(mass);
+    }
+    mass_all += mass;
+    if (lane == 0) chunk_mass[ch] = mass;
+    if (lane < parts) cluster.map_shared_rank(states, lane)[part * a.per + ch] = st;
+  }
+  if (keep && threadIdx.x == 0 && v0 + n == V)  // the last word's bytes past V
+    for (int b = (V + 7) / 8; b < a.words * 4; ++b) keep[b] = 0;
+  const uint64_t mine = block_sum(s, lane == 0 ? mass_all : 0);
+  const int kept = static_cast<int>(block_sum(s, count));
+  if (threadIdx.x < static_cast<unsigned>(parts)) {
+    FilterShared* o = cluster.map_shared_rank(&s, threadIdx.x);
+    o->part_a[part] = mine;
+    o->part_n[part] = kept;
+  }
+  cluster.sync();
+  uint64_t total = 0, before = 0;
+  int kept_all = 0;
+  for (int i = 0; i < parts; ++i) {
+    if (i < part) before += s.part_a[i];
+    total += s.part_a[i];
+    kept_all += s.part_n[i];
+  }
+  bool exact;
+  uint64_t r = first ? 0 : mul_frac(total, u, &exact);  // the token: running sum > u * total
+  if (r < before || r - before >= mine) return;  // (nobody writes to this CTA any more)
+  r -= before;
+
+  // ---- the chunk, then the column
+  if (warp == 0) {
+    uint64_t at = 0;
+    for (int c0 = 0;; c0 += 32) {
+      const uint64_t x = c0 + lane < own_chunks ? chunk_mass[c0 + lane] : 0;
+      uint64_t inc = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const uint32_t b = __ballot_sync(0xffffffffu, at + inc > r);
+      if (b || c0 + 32 >= own_chunks) {
+        if (lane == (b ? __ffs(b) - 1 : 0)) {
+          s.hit = c0 + lane;
+          s.rest = r - (at + inc - x);
+        }
+        break;
+      }
+      at += __shfl_sync(0xffffffffu, inc, 31);
+    }
   }
   __syncthreads();
-  if (warp != s.warp) return;
-  const float2 st = keep_merge(states, a.chunks, c);
-  uint64_t r = s.rest;
-  for (int v = v0; v < v1; v += 32) {
-    uint64_t w = 0;
-    float x = 0.f;
-    if (v + lane < v1) {
-      x = to_f32(z[v + lane]);
-      if (cut.has(x, v + lane)) w = first ? 1 : fix_weight(scale, s.table, x);
-    }
-    uint64_t inc = w;
+  const int base = s.hit * kKeepChunk;
+  r = s.rest;
+  constexpr int kCols = kKeepChunk / kFilterThreads;
+  uint64_t w[kCols], sum = 0, all;
+  float x[kCols];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
+  for (int q = 0; q < kCols; ++q) {
+    const int i = base + threadIdx.x * kCols + q;
+    w[q] = 0;
+    x[q] = 0.f;
+    if (i < n) {
+      x[q] = to_f32(z[i]);
+      if (cut.has(x[q], v0 + i)) w[q] = first ? 1 : fix_weight(scale, s.table, x[q]);
     }
-    const uint32_t b = __ballot_sync(0xffffffffu, inc > r);
-    if (b) {
-      if (lane == __ffs(b) - 1) {
-        a.tokens[row] = v + lane;
-        a.logprob[row] = keep_logprob_of(x, st, tau);
-        if (a.kept) a.kept[row] = s.n;
+    sum += w[q];
+  }
+  uint64_t at = block_scan(s.red, sum, all);
+  if (r >= at && r < at + sum) {
+#pragma unroll
+    for (int q = 0; q < kCols; ++q) {
+      if (r >= at && r < at + w[q]) {
+        a.tokens[row] = v0 + base + threadIdx.x * kCols + q;
+        s.redf[0] = x[q];
       }
-      break;
+      at += w[q];
     }
-    r -= __shfl_sync(0xffffffffu, inc, 31);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const float2 st = keep_merge(states, a.chunks, c);
+    if (lane == 0) {
+      a.logprob[row] = keep_logprob_of(s.redf[0], st, tau);
+      if (a.kept) a.kept[row] = kept_all;
+    }
   }
 }
 
-template <class E>
-cudaError_t launch(const FilterArgs& a, int64_t T, cudaStream_t st) {
-  const size_t smem = (sizeof(FilterShared) + 15) / 16 * 16 +
-                      static_cast<size_t>(a.chunks) * sizeof(float2);
-  cudaError_t e = cudaFuncSetAttribute(filter_sample_kernel<E>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 131072);
+template <class E, bool kResident>
+cudaError_t launch_as(const FilterArgs& a, int64_t T, int parts, size_t smem, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(filter_sample_kernel<E, kResident>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(kSmemLimit));
   if (e != cudaSuccess) return e;
-  filter_sample_kernel<E><<<static_cast<unsigned>(T), kFilterThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(T * parts));
+  cfg.blockDim = dim3(kFilterThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = parts;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, filter_sample_kernel<E, kResident>, a);
+}
+
+template <class E>
+cudaError_t launch(FilterArgs a, int64_t T, cudaStream_t st) {
+  // CTAs to a row: what lets two CTAs share an SM with their slices; more, up
+  // to eight, while the rows do not fill the GPU twice
+  const auto per = [&](int parts) { return (a.chunks + parts - 1) / parts; };
+  const auto bytes = [&](int parts) {
+    return static_cast<size_t>(per(parts)) * kKeepChunk * sizeof(E);
+  };
+  int parts = 1;
+  while (parts < kMaxParts && (bytes(parts) > kSliceMax || T * parts < 2 * num_sms()) &&
+         parts < a.chunks)
+    parts *= 2;
+  a.per = per(parts);
+  const size_t fixed = ((sizeof(FilterShared) + 15) / 16 * 16 +
+                        static_cast<size_t>(a.chunks + a.per) * 8 + 127) / 128 * 128;
+  if (fixed + bytes(parts) <= kSmemLimit)
+    return launch_as<E, true>(a, T, parts, fixed + bytes(parts), st);
+  return launch_as<E, false>(a, T, parts, fixed, st);
 }
 
 }  // namespace
@@ -381,7 +921,7 @@ extern "C" int rz_filter_sample(const void* logits, int64_t ld, int32_t dtype, i
                                 const float* top_p, const float* min_p, const float* uniform,
                                 int32_t* tokens_out, float* logprob_out, int32_t* kept_out,
                                 uint32_t* keep_out, int32_t* err_flag, rz_stream_t stream) {
-  if (T < 0 || T >= (int64_t(1) << 31) - 1 || V < 1 || V > (1 << 24)) return RZ_ERR_INVALID_ARG;
+  if (T < 0 || T >= (int64_t(1) << 28) || V < 1 || V > (1 << 24)) return RZ_ERR_INVALID_ARG;
   if (dtype != RZ_DTYPE_F32 && dtype != RZ_DTYPE_BF16 && dtype != RZ_DTYPE_F16)
     return RZ_ERR_INVALID_ARG;
   if (ld < V || (T > 0 && (!logits || !uniform || !tokens_out || !logprob_out)))
@@ -390,9 +930,9 @@ extern "C" int rz_filter_sample(const void* logits, int64_t ld, int32_t dtype, i
     return RZ_ERR_UNSUPPORTED;
   if (T == 0) return RZ_OK;
   if (!device_ok()) return RZ_ERR_UNSUPPORTED;
-  FilterArgs a{logits,     ld,          temperature, top_k,    top_p, min_p,
-               uniform,    tokens_out,  logprob_out, kept_out, keep_out, err_flag,
-               V, (V + 31) / 32, (V + kKeepChunk - 1) / kKeepChunk, fix_bits(V)};
+  FilterArgs a{logits,  ld,         temperature, top_k,    top_p,    min_p,
+               uniform, tokens_out, logprob_out, kept_out, keep_out, err_flag,
+               V, (V + 31) / 32, (V + kKeepChunk - 1) / kKeepChunk, fix_bits(V), 0};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(RZ_PROF_LOGITS_ROWS, 1, st);
   const cudaError_t e = dtype == RZ_DTYPE_F32    ? launch<float>(a, T, st)

@@ -10,20 +10,18 @@
 // arithmetic.
 //
 // A row is read from memory once: a cluster of up to eight CTAs holds it in
-// shared memory, a slice of whole 2,048-column chunks each, and passes over it
+// shared memory, a slice of whole 1,024-column chunks each, and passes over it
 //   1  while it arrives: its maximum and minimum;
 //   2  (top-k, top-p) counts in 2,048 bins linear in y = (max - z) log2(e) / tau;
 //      from the counts and the bins' edges follow the bin of the k-th logit
 //      and, as bounds on every mass, the few bins that top-p's border can be in;
 //   3  (top-p) the exact masses above and below those bins; (both) what is in
-//      them goes to a list, in which the first CTA finds the border by 8 bits
-//      of the key at a time (a list that overflows: the same over the row);
-//   4  the kept set's bits, the log-sum-exp as the learner takes it, the kept
-//      mass of each chunk; then the chunk and the column where the running sum
-//      passes u.
-// A pass costs 5 to 10 instructions a logit, an exact weight 35.  That bounds
-// a large batch, not the memory: the weight is evaluated once a logit for
-// top-p, and again only for what is kept.
+//      them goes to a list of the first CTA, which sorts it and adds up its
+//      masses in that order (a list that overflows, as with very many equal
+//      logits: 8 bits of the key at a time over the row);
+//   4  the kept set's bits, the log-sum-exp as the learner takes it and, where
+//      pass 3 has not, the mass of each 256 columns; then the 256 columns and
+//      the one of them where the running sum passes u.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -43,8 +41,8 @@ constexpr int kFilterThreads = 512;
 constexpr int kFilterWarps = kFilterThreads / 32;
 constexpr int kMaxParts = 8;      // CTAs of a row
 constexpr int kBins = 2048;
-constexpr int kOwnList = 512;     // list entries of one CTA
-constexpr int kList = 1024;       // of the row
+constexpr int kList = 2048;       // entries that are sorted, not searched for
+constexpr int kBlock = 256;       // columns to a mass
 constexpr size_t kSliceMax = 81920;  // two CTAs an SM
 constexpr size_t kSmemLimit = 232448;  // of a CTA alone on its SM
 
@@ -75,63 +73,69 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 constexpr uint32_t kKeyNegInf = 0x007fffffu;  // order_key(-inf)
 
-// The kept head: key > t, or key = t and index <= last.
+// The kept head: z > t, or z = t and index <= last.
 struct Cut {
-  uint32_t t;
+  float t;
   int last;
   __device__ __forceinline__ bool has(float z, int v) const {
-    const uint32_t k = order_key(z);
-    return k > t || (k == t && v <= last);
+    return z > t || (z == t && v <= last);
   }
 };
 
-// x * (f * 2^64) / 2^64, floor, for a float 0 <= f < 1; *exact = no remainder.
-__device__ __forceinline__ uint64_t mul_frac(uint64_t x, float f, bool* exact) {
-  const uint64_t m = static_cast<uint64_t>(static_cast<double>(f) * 18446744073709551616.0);
-  *exact = x * m == 0;
-  return __umul64hi(x, m);
+// f 2^64 for a float 0 <= f < 1 (rounded down below 2^-40), from its bits.
+__device__ __forceinline__ uint64_t frac64(float f) {
+  const uint32_t u = __float_as_uint(f);
+  const int e = static_cast<int>(u >> 23);
+  if (e == 0) return 0;
+  const uint64_t m = (u & 0x7fffffu) | 0x800000u;
+  return e >= 86 ? m << (e - 86) : (86 - e < 24 ? m >> (86 - e) : 0);
 }
-// Smallest integer >= p * x, at least 1: a token is in while the mass above it
-// is less than this.
-__device__ __forceinline__ uint64_t mass_target(uint64_t x, float p) {
-  bool exact = true;
-  uint64_t t = p > 0.f ? mul_frac(x, p, &exact) : 0;
-  if (!exact || t == 0) ++t;
-  return t;
+// Smallest integer >= p x, at least 1 (p = f / 2^64): a token is in while the
+// mass above it is less than this.
+__device__ __forceinline__ uint64_t mass_target(uint64_t x, uint64_t f) {
+  const uint64_t t = __umul64hi(x, f) + (x * f != 0);
+  return t > 0 ? t : 1;
 }
 
-struct Entry {
-  uint32_t key;
-  int idx;
-};
+// A list entry orders as the row does: the key, then the lower index.
+__device__ __forceinline__ uint64_t entry_of(float z, int v) {
+  return static_cast<uint64_t>(order_key(z)) << 32 | static_cast<uint32_t>(~v);
+}
+__device__ __forceinline__ float entry_value(uint64_t e) {
+  return key_value(static_cast<uint32_t>(e >> 32));
+}
+__device__ __forceinline__ int entry_index(uint64_t e) {
+  return static_cast<int>(~static_cast<uint32_t>(e));
+}
 
 struct FilterShared {
-  uint64_t table[kFixTable];
+  uint32_t table[kFixTable];
   union {
     uint32_t bins[kBins];
-    Entry list[kList];  // (first CTA) once the bins have been read
-  };
-  union {
-    Entry own[kOwnList];
+    uint64_t list[kList];  // (first CTA) once the bins have been read
     struct {
       uint32_t count[256], lo[256], hi[256];
-    } digit;
+    } digit;            // once the list has overflowed
   };
   uint64_t red[kFilterWarps];
   float redf[2 * kFilterWarps];
   // written by every CTA of the cluster
   float part_max[kMaxParts], part_min[kMaxParts];
-  int part_nan[kMaxParts], part_list[kMaxParts], part_n[kMaxParts];
+  int part_nan[kMaxParts], part_n[kMaxParts];
   uint64_t part_a[kMaxParts], part_b[kMaxParts];
+  int listed;  // (first CTA)
   // written by the first CTA
-  int bin_k, bin_lo, bin_hi;
+  int bin_k, bin_lo, bin_hi, n_list;
   uint32_t above_k;
-  uint32_t cut_t;
+  float cut_t;
   int cut_last;
   uint32_t digit_now;
   uint64_t above;
+  // the row's parameters, by one thread of each CTA
+  float c_hi, c_lo;
+  double min_p_reach;
   // scratch
-  int own_n, hit;
+  int hit, top;
   uint64_t rest;
 };
 
@@ -175,10 +179,29 @@ __device__ __forceinline__ Tv block_scan(Tv* scratch, Tv x, Tv& total) {
   return base + inc - x;
 }
 
+// Descending sort of s.list[0 .. size) by the block, size a power of two of at
+// least 64: a bitonic network, a warp's pairs within the same 64 entries
+// wherever the stride allows, so that most steps need no block barrier.
+__device__ void sort_list(FilterShared& s, int size) {
+  for (int k = 2; k <= size; k <<= 1) {
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      for (int p = threadIdx.x; p < size / 2; p += kFilterThreads) {
+        const int i = (p & ~(j - 1)) * 2 + (p & (j - 1));
+        const uint64_t x = s.list[i], y = s.list[i + j];
+        if ((x < y) == ((i & k) == 0)) {
+          s.list[i] = y;
+          s.list[i + j] = x;
+        }
+      }
+      if (j > 32 || (j == 1 && k >= 64)) __syncthreads();
+      else __syncwarp();
+    }
+  }
+}
+
 // ------------------------------------------------------------------ selection
 // The largest key t such that the keys >= t have a count (or mass) of at least
-// `target`, and what lies above it, 8 bits at a time.  What is looked through:
-// the row's logits (every CTA takes part) or the list (the first CTA).
+// `target`, and what lies above it, 8 bits at a time.
 enum Measure { kCount, kMass, kIndex };  // kIndex: count, of the keys ~index
 
 __device__ __forceinline__ void digit_add(FilterShared& s, uint32_t b, uint64_t w, bool mass) {
@@ -223,40 +246,6 @@ __device__ __forceinline__ void digit_find(FilterShared& s, uint64_t target, uin
     s.digit_now = 255 - 8 * lane - i;
     s.above = a;
   }
-}
-
-// Over the list of n entries, first CTA only.  floor: smaller keys are left out;
-// equal: (kIndex) only entries of this key.
-__device__ void select_list(FilterShared& s, const FixScale& scale, Measure what, int n,
-                            uint32_t floor, uint32_t equal, uint64_t target, uint32_t& t_out,
-                            uint64_t& above_out) {
-  uint32_t prefix = 0;
-  uint64_t above = 0;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kFilterThreads)
-      s.digit.count[i] = s.digit.lo[i] = s.digit.hi[i] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kFilterThreads) {
-      const Entry e = s.list[i];
-      const uint32_t k = what == kIndex ? ~static_cast<uint32_t>(e.idx) : e.key;
-      if (what == kIndex ? e.key != equal : e.key < floor) continue;
-      if (shift < 24 && (k >> (shift + 8)) != prefix) continue;
-      digit_add(s, (k >> shift) & 255u,
-                what == kMass ? fix_weight(scale, s.table, key_value(e.key)) : 1, what == kMass);
-    }
-    __syncthreads();
-    if (threadIdx.x < 32)
-      digit_find(s, target, above, [&](int b) {
-        return what == kMass ? (static_cast<uint64_t>(s.digit.hi[b]) << 32) + s.digit.lo[b]
-                             : static_cast<uint64_t>(s.digit.count[b]);
-      });
-    __syncthreads();
-    prefix = prefix << 8 | s.digit_now;
-    above = s.above;
-  }
-  __syncthreads();
-  t_out = prefix;
-  above_out = above;
 }
 
 // Over the row: every CTA of the cluster looks through its slice z (columns
@@ -338,21 +327,29 @@ struct Binning {
     const float y = __fmul_rn(__fsub_rn(zmax, z), c_hi);
     return static_cast<int>(fminf(__fmul_rn(y, scale), static_cast<float>(kBins - 1)));
   }
-  // Bounds on the weight of what is in bin b: the table's steps of 2^-11 just
-  // outside of it (and one more for the roundings of y).
-  __device__ __forceinline__ uint64_t most(const uint64_t* tab, int drop, int b) const {
-    const int k = static_cast<int>(floorf(b / scale * kFixTable)) - 2;
+  // Bounds on the weight of what is in bin b: the table's steps of 2^-10 just
+  // outside of it (and one more for the roundings of y).  per = steps a bin.
+  __device__ __forceinline__ uint64_t most(const uint32_t* tab, int drop, float per, int b) const {
+    const int k = static_cast<int>(b * per) - 2;
     return at(tab, drop, k < 0 ? 0 : k) + 1;
   }
-  __device__ __forceinline__ uint64_t least(const uint64_t* tab, int drop, int b) const {
+  __device__ __forceinline__ uint64_t least(const uint32_t* tab, int drop, float per,
+                                            int b) const {
     if (b == kBins - 1) return 0;
-    return at(tab, drop, static_cast<int>(ceilf((b + 1) / scale * kFixTable)) + 2);
+    return at(tab, drop, static_cast<int>((b + 1) * per) + 3);
   }
-  static __device__ __forceinline__ uint64_t at(const uint64_t* tab, int drop, int k) {
+  static __device__ __forceinline__ uint64_t at(const uint32_t* tab, int drop, int k) {
     const int sh = (k >> kFixTableBits) + drop;
-    return sh > 60 ? 0 : (tab[k & (kFixTable - 1)] >> sh) >> 1;
+    return sh > 62 ? 0 : ((static_cast<uint64_t>(tab[k & (kFixTable - 1)]) << 32) >> sh) >> 1;
   }
 };
+
+// Shared memory ahead of the slice: FilterShared, the chunks' states, the own
+// columns' masses.
+__host__ __device__ constexpr size_t filter_fixed_bytes(int chunks, int per) {
+  return ((sizeof(FilterShared) + 15) / 16 * 16 + chunks * 8 +
+          static_cast<size_t>(per) * (kKeepChunk / kBlock) * 8 + 127) / 128 * 128;
+}
 
 template <class E, bool kResident>
 __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
@@ -360,10 +357,10 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
   extern __shared__ uint8_t smem[];
   FilterShared& s = *reinterpret_cast<FilterShared*>(smem);
   float2* states = reinterpret_cast<float2*>(smem + (sizeof(FilterShared) + 15) / 16 * 16);
-  uint64_t* chunk_mass = reinterpret_cast<uint64_t*>(states + a.chunks);  // own chunks
-  E* slice = reinterpret_cast<E*>(smem + ((sizeof(FilterShared) + 15) / 16 * 16 +
-                                          (a.chunks + a.per) * 8 + 127) / 128 * 128);
+  uint64_t* block_mass = reinterpret_cast<uint64_t*>(states + a.chunks);  // own columns
+  E* slice = reinterpret_cast<E*>(smem + filter_fixed_bytes(a.chunks, a.per));
   cg::cluster_group cluster = cg::this_cluster();
+  cluster.barrier_arrive();  // (waited for before another CTA's memory is written)
   const int parts = static_cast<int>(cluster.num_blocks());
   const int part = static_cast<int>(cluster.block_rank());
   const bool lead = part == 0;
@@ -385,7 +382,19 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
   };
   for (int i = threadIdx.x; i < kFixTable; i += kFilterThreads) s.table[i] = g_fix_table.v[i];
   for (int i = threadIdx.x; i < kBins; i += kFilterThreads) s.bins[i] = 0;
-  if (threadIdx.x == 0) s.own_n = 0;
+  const float temperature = a.temperature ? a.temperature[row] : 1.f;
+  const float tau = row_tau(a.temperature, row);
+  const float u = a.uniform[row];
+  const float p = a.top_p ? a.top_p[row] : 1.f;
+  const float mp = a.min_p ? a.min_p[row] : 0.f;
+  if (threadIdx.x == 0) {
+    s.listed = 0;
+    // (fp64 by one thread: two such operations a clock are what an SM has)
+    const double c = 1.44269504088896340736 / static_cast<double>(tau);
+    s.c_hi = static_cast<float>(c);
+    s.c_lo = static_cast<float>(c - static_cast<double>(s.c_hi));
+    s.min_p_reach = mp > 0.f ? static_cast<double>(tau) * log(static_cast<double>(mp)) : 0.0;
+  }
   {
     const E* src = zrow + v0;
     constexpr int kPer = 16 / sizeof(E);
@@ -424,7 +433,7 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
     s.redf[kFilterWarps + warp] = mn;
   }
   const int any_nan = __syncthreads_or(nan);
-  if (parts > 1) cluster.sync();  // every CTA runs before its memory is written
+  cluster.barrier_wait();  // every CTA runs
   if (threadIdx.x < static_cast<unsigned>(parts)) {
     mx = s.redf[0];
     mn = s.redf[kFilterWarps];
@@ -446,11 +455,6 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
     bad_logits |= s.part_nan[i];
   }
 
-  const float temperature = a.temperature ? a.temperature[row] : 1.f;
-  const float tau = row_tau(a.temperature, row);
-  const float u = a.uniform[row];
-  const float p = a.top_p ? a.top_p[row] : 1.f;
-  const float mp = a.min_p ? a.min_p[row] : 0.f;
   int k = a.top_k ? a.top_k[row] : 0;
   if (k <= 0 || k > V) k = V;
   if (temperature == 0.f) k = 1;
@@ -470,29 +474,24 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
     return;  // the whole cluster does; nobody's memory is in use
   }
   FixScale scale;
-  {
-    const double c = 1.44269504088896340736 / static_cast<double>(tau);
-    scale.zmax = zmax;
-    scale.c_hi = static_cast<float>(c);
-    scale.c_lo = static_cast<float>(c - static_cast<double>(scale.c_hi));
-    scale.drop = kFixQ - a.fix_bits;
-  }
+  scale.zmax = zmax;
+  scale.c_hi = s.c_hi;
+  scale.c_lo = s.c_lo;
+  scale.bits(a.fix_bits);
 
   // ---- 2, 3: the cut
-  uint32_t t = kKeyNegInf;  // key > t, or one of the first `ties` at key = t
-  long long ties = 0;
-  int last = -1;
+  Cut cut{-INFINITY, -1};
+  bool have_mass = false;  // block_mass holds the kept mass of the own columns
   const bool want_k = k < V, want_p = p < 1.f;
   if (want_k || want_p) {
+    const uint64_t pf = want_p && p > 0.f ? frac64(p) : 0;
     Binning bn;
     bn.zmax = zmax;
     bn.c_hi = scale.c_hi;
-    {
-      // 2,048 bins over the row's range, at most 32 (in y; what is beyond
-      // weighs nothing) and no finer than the table
-      const float range = __fmul_rn(__fsub_rn(zmax, zmin), scale.c_hi);
-      bn.scale = (kBins - 2) / fminf(fmaxf(range, 1.f), 32.f);
-    }
+    // 2,048 bins over the row's range, at most 32 (in y; what is beyond weighs
+    // next to nothing) and no finer than the table
+    const float range = fminf(fmaxf(__fmul_rn(__fsub_rn(zmax, zmin), scale.c_hi), 2.f), 32.f);
+    bn.scale = (kBins - 2) / range;
     for (int i = threadIdx.x; i < n; i += kFilterThreads) {
       const float x = to_f32(z[i]);
       if (x > -INFINITY) atomicAdd(&s.bins[bn.bin(x)], 1u);
@@ -534,14 +533,15 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
       if (want_p) {
         // bounds on the masses of the bins, in top-k's head
         const int bin_k = s.bin_k;
+        const float per = range * (static_cast<float>(kFixTable) / (kBins - 2));
         uint64_t lo[kEach], hi[kEach], lo_sum = 0, hi_sum = 0, lo_all, hi_all;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
           const int b = b0 + i;
           const uint32_t m = b < bin_k ? c[i] : (b == bin_k ? k - s.above_k : 0u);
           c[i] = m;
-          lo[i] = m ? m * bn.least(s.table, scale.drop, b) : 0;
-          hi[i] = m ? m * bn.most(s.table, scale.drop, b) : 0;
+          lo[i] = m ? m * bn.least(s.table, scale.drop, per, b) : 0;
+          hi[i] = m ? m * bn.most(s.table, scale.drop, per, b) : 0;
           lo_sum += lo[i];
           hi_sum += hi[i];
         }
@@ -553,8 +553,8 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
             // may what lies above be short of p of all, and may what lies
             // above and here reach it?
             const uint64_t lo_end = lo_at + lo[i], hi_end = hi_at + hi[i];
-            if (lo_at < mass_target(lo_at + (hi_all - hi_at), p) &&
-                hi_end >= mass_target(hi_end + (lo_all - lo_end), p)) {
+            if (lo_at < mass_target(lo_at + (hi_all - hi_at), pf) &&
+                hi_end >= mass_target(hi_end + (lo_all - lo_end), pf)) {
               atomicMin(&s.bin_lo, b0 + i);
               atomicMax(&s.bin_hi, b0 + i);
             }
@@ -573,112 +573,144 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
       }
     }
     if (parts > 1) cluster.sync();
+    else __syncthreads();
     const int bin_k = s.bin_k, bin_lo = s.bin_lo, bin_hi = s.bin_hi;
     const bool cut_k = bin_k < kBins;
-    // the exact masses above the band, and of all of top-k's head but the
-    // band and bin_k; what is in these two is listed
+    // the exact masses above the band, by blocks, and of the rest of top-k's
+    // head but the band and bin_k; what is in these two is listed
+    FilterShared* first_cta = cluster.map_shared_rank(&s, 0);
+    const bool vec = kResident || row_aligned(z);
     uint64_t sum_a = 0, sum_r = 0;
-    for (int i = threadIdx.x; i < n; i += kFilterThreads) {
-      const float x = to_f32(z[i]);
-      const int b = bn.bin(x);
-      if (b > bin_k || !(x > -INFINITY)) continue;
-      if ((want_p && b >= bin_lo && b <= bin_hi) || b == bin_k) {
-        const int at = atomicAdd(&s.own_n, 1);
-        if (at < kOwnList) {
-          s.own[at].key = order_key(x);
-          s.own[at].idx = v0 + i;
+    for (int blk = warp; blk * kBlock < n; blk += kFilterWarps) {
+      const int i = blk * kBlock + 8 * lane;
+      uint64_t mass = 0;
+      if (i < n) {
+        float v[8];
+        load8(z, vec, n, i, v);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float x = v[q];
+          const int b = bn.bin(x);
+          if (b > bin_k || !(x > -INFINITY)) continue;
+          const bool listed = (b >= bin_lo && b <= bin_hi) || b == bin_k;
+          if (!listed && !want_p) continue;
+          if (listed) {
+            const int at = atomicAdd(&first_cta->listed, 1);
+            if (at < kList) first_cta->list[at] = entry_of(x, v0 + i + q);
+          } else {
+            const uint64_t w = fix_weight(scale, s.table, x);
+            if (b < bin_lo) mass += w;
+            else sum_r += w;
+          }
         }
-      } else if (want_p) {
-        const uint64_t w = fix_weight(scale, s.table, x);
-        if (b < bin_lo) sum_a += w;
-        else sum_r += w;
+      }
+      if (want_p) {
+        mass = warp_sum(mass);
+        if (lane == 0) {
+          block_mass[blk] = mass;
+          sum_a += mass;
+        }
       }
     }
     if (want_p) {
       sum_a = block_sum(s, sum_a);
       sum_r = block_sum(s, sum_r);
-    } else {
-      __syncthreads();
-    }
-    const int own = s.own_n;
-    if (threadIdx.x < static_cast<unsigned>(parts)) {
-      FilterShared* o = cluster.map_shared_rank(&s, threadIdx.x);
-      o->part_a[part] = sum_a;
-      o->part_b[part] = sum_r;
-      o->part_list[part] = own;
+      if (threadIdx.x < static_cast<unsigned>(parts)) {
+        FilterShared* o = cluster.map_shared_rank(&s, threadIdx.x);
+        o->part_a[part] = sum_a;
+        o->part_b[part] = sum_r;
+      }
     }
     cluster.sync();
-    int listed = 0, offset = 0;
-    bool fits = true;
-    for (int i = 0; i < parts; ++i) {
-      if (i < part) offset += s.part_list[i];
-      fits = fits && s.part_list[i] <= kOwnList;
-      listed += s.part_list[i];
-    }
-    fits = fits && listed <= kList;
-    if (fits) {
-      Entry* list = cluster.map_shared_rank(&s, 0)->list;
-      for (int i = threadIdx.x; i < own; i += kFilterThreads) list[offset + i] = s.own[i];
-      cluster.sync();
-      if (lead) {
-        uint64_t above;
+    if (lead) {
+      const int listed = s.listed;
+      if (listed <= kList) {
+        int size = 64;
+        while (size < listed) size *= 2;
+        for (int i = listed + threadIdx.x; i < size; i += kFilterThreads) s.list[i] = 0;
+        __syncthreads();
+        sort_list(s, size);
+        constexpr int kEach = kList / kFilterThreads;
+        const int e0 = threadIdx.x * kEach;
+        uint64_t e[kEach], w[kEach], sum = 0, all;
+        int over = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          e[i] = e0 + i < listed ? s.list[e0 + i] : 0;
+          if (cut_k) over += e0 + i < listed && bn.bin(entry_value(e[i])) < bin_k;
+        }
+        // how many are in by the count (the list holds whole bins: those above
+        // bin_k are among above_k)
+        int in = listed;
         if (cut_k) {
-          // (entries of the band above bin_k are above every key of bin_k)
-          uint32_t tk;
-          uint64_t extra = 0;  // listed entries in bins above bin_k
-          {
-            int c = 0;
-            for (int i = threadIdx.x; i < listed; i += kFilterThreads)
-              c += bn.bin(key_value(s.list[i].key)) < bin_k;
-            extra = block_sum(s, c);
-          }
-          select_list(s, scale, kCount, listed, 0u, 0u, k - s.above_k + extra, tk, above);
-          t = tk;
-          ties = static_cast<long long>(k - s.above_k + extra - above);
+          int over_all;
+          block_scan(reinterpret_cast<int*>(s.red), over, over_all);
+          in = min(listed, static_cast<int>(k - s.above_k) + over_all);
+        }
+        if (threadIdx.x == 0) {
+          s.top = in;
+          s.cut_t = -INFINITY;  // nothing listed: no cut
+          s.cut_last = -1;
         }
         if (want_p) {
-          uint64_t base = 0, total = 0;
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) {
+            w[i] = e0 + i < in ? fix_weight(scale, s.table, entry_value(e[i])) : 0;
+            sum += w[i];
+          }
+          uint64_t at = block_scan(s.red, sum, all);
+          uint64_t base = 0, total = all;
           for (int i = 0; i < parts; ++i) {
             base += s.part_a[i];
             total += s.part_a[i] + s.part_b[i];
           }
-          // the listed part of top-k's head
-          uint64_t x = 0;
-          for (int i = threadIdx.x; i < listed; i += kFilterThreads) {
-            const uint32_t key = s.list[i].key;
-            if (key > t) x += fix_weight(scale, s.table, key_value(key));
+          const uint64_t target = mass_target(total, pf);
+          at += base;
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) {
+            // the first that is not in, its mass above reaching the target
+            if (e0 + i < in) {
+              if (at >= target) {
+                atomicMin(&s.top, e0 + i);
+              } else {
+                const int blk = entry_index(e[i]) / kBlock, per = a.per * (kKeepChunk / kBlock);
+                atomicAdd(reinterpret_cast<unsigned long long*>(
+                              cluster.map_shared_rank(block_mass, blk / per) + blk % per),
+                          static_cast<unsigned long long>(w[i]));
+              }
+            }
+            at += w[i];
           }
-          total += block_sum(s, x);
-          if (ties > 0) total += ties * fix_weight(scale, s.table, key_value(t));
-          const uint64_t target = mass_target(total, p);
-          uint32_t tp;
-          select_list(s, scale, kMass, listed, ties > 0 ? t : t + 1, 0u, target - base, tp, above);
-          const uint64_t w = fix_weight(scale, s.table, key_value(tp));
-          long long m = w > 0 ? static_cast<long long>((target - base - above + w - 1) / w) : 1;
-          if (tp == t && m > ties) m = ties;
-          t = tp;
-          ties = m;
         }
-        if (ties > 0) {
-          uint32_t at;
-          select_list(s, scale, kIndex, listed, 0u, t, ties, at, above);
-          last = static_cast<int>(~at);
+        __syncthreads();
+        if (threadIdx.x == 0 && listed > 0) {
+          // the last that is in, or (none) the first listed, left out
+          const uint64_t x = s.list[s.top > 0 ? s.top - 1 : 0];
+          s.cut_t = entry_value(x);
+          s.cut_last = s.top > 0 ? entry_index(x) : -1;
         }
-        if (threadIdx.x < static_cast<unsigned>(parts)) {
-          FilterShared* o = cluster.map_shared_rank(&s, threadIdx.x);
-          o->cut_t = t;
-          o->cut_last = last;
+        __syncthreads();
+      }
+      if (threadIdx.x < static_cast<unsigned>(parts)) {
+        FilterShared* o = cluster.map_shared_rank(&s, threadIdx.x);
+        o->n_list = listed;
+        if (threadIdx.x != 0) {
+          o->cut_t = s.cut_t;
+          o->cut_last = s.cut_last;
         }
       }
-      cluster.sync();
-      t = s.cut_t;
-      last = s.cut_last;
+    }
+    cluster.sync();
+    if (s.n_list <= kList) {
+      cut = Cut{s.cut_t, s.cut_last};
+      have_mass = want_p;
     } else {
       // more in the bins than the list holds: the same over the row
-      uint64_t above;
+      uint32_t t = kKeyNegInf;  // key > t, or one of the first `ties` at key = t
+      uint64_t above, ties = 0;
       if (cut_k) {
         select_row(s, cluster, scale, kCount, z, v0, n, 0u, 0u, k, t, above);
-        ties = k - static_cast<long long>(above);
+        ties = k - above;
       }
       if (want_p) {
         uint64_t x = 0;
@@ -693,47 +725,43 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
         uint64_t total = 0;
         for (int i = 0; i < parts; ++i) total += s.part_a[i];
         if (ties > 0) total += ties * fix_weight(scale, s.table, key_value(t));
-        const uint64_t target = mass_target(total, p);
+        const uint64_t target = mass_target(total, pf);
         uint32_t tp;
         select_row(s, cluster, scale, kMass, z, v0, n, ties > 0 ? t : t + 1, 0u, target, tp, above);
         const uint64_t w = fix_weight(scale, s.table, key_value(tp));
-        long long m = w > 0 ? static_cast<long long>((target - above + w - 1) / w) : 1;
+        uint64_t m = w > 0 ? (target - above + w - 1) / w : 1;
         if (tp == t && m > ties) m = ties;
         t = tp;
         ties = m;
       }
-      if (ties > 0) {
-        uint32_t at;
-        select_row(s, cluster, scale, kIndex, z, v0, n, 0u, t, ties, at, above);
-        last = static_cast<int>(~at);
-      }
+      uint32_t at;
+      select_row(s, cluster, scale, kIndex, z, v0, n, 0u, t, ties, at, above);
+      cut = Cut{key_value(t), static_cast<int>(~at)};
     }
   }
   if (mp > 0.f) {
-    const float zlow = __double2float_ru(static_cast<double>(zmax) +
-                                         static_cast<double>(tau) * log(static_cast<double>(mp)));
-    const uint32_t km = order_key(zlow);
-    if (km > t) {
-      t = km - 1;
-      last = -1;
+    const float zlow = __double2float_ru(static_cast<double>(zmax) + s.min_p_reach);
+    if (zlow > cut.t) {
+      cut = Cut{zlow, V};
+      have_mass = false;
     }
   }
-  const Cut cut{t, last};
 
-  // ---- 4: kept bits, log-sum-exp and mass of each chunk (the two passes of
-  // keep_fold, a warp a chunk, with its operations in its order)
+  // ---- 4: kept bits, log-sum-exp and masses (the two passes of keep_fold, a
+  // warp a chunk, with its operations in its order)
   const float c = keep_scale(tau);
   const bool vec = kResident || row_aligned(z);
   const bool first = u == 0.f;  // the first kept token, whatever its weight rounds to
+  have_mass = have_mass && !first;
   uint8_t* keep = a.keep ? reinterpret_cast<uint8_t*>(a.keep + row * a.words) : nullptr;
   int count = 0;
   const int own_chunks = (n + kKeepChunk - 1) / kKeepChunk;
-  uint64_t mass_all = 0;
+  uint64_t mine = 0;
   for (int ch = warp; ch < own_chunks; ch += kFilterWarps) {
-    uint32_t bits[2] = {0u, 0u};
+    uint32_t bits = 0;  // 8 for each step
     float m = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < kKeepSteps; ++j) {
       const int i = ch * kKeepChunk + 256 * j + 8 * lane;
       if (i < n) {
         float v[8];
@@ -741,26 +769,26 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
         uint32_t b = 0;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          if (i + q < n && cut.has(v[q], v0 + i + q)) {
+          if (cut.has(v[q], v0 + i + q)) {  // (load8 gives -inf past the end)
             b |= 1u << q;
             m = fmaxf(m, v[q]);
           }
         }
-        bits[j >> 2] |= b << (8 * (j & 3));
+        bits |= b << (8 * j);
         if (keep) keep[(v0 + i) >> 3] = static_cast<uint8_t>(b);
       }
     }
-    count += __popc(bits[0]) + __popc(bits[1]);
+    count += __popc(bits);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float2 st = make_float2(-INFINITY, 0.f);
-    uint64_t mass = 0;
     if (m > -INFINITY) {
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
       int top = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t b = (bits[j >> 2] >> (8 * (j & 3))) & 255u;
+      for (int j = 0; j < kKeepSteps; ++j) {
+        const uint32_t b = (bits >> (8 * j)) & 255u;
+        uint64_t mass = 0;
         if (b) {
           float v[8];
           load8(z, vec, n, ch * kKeepChunk + 256 * j + 8 * lane, v);
@@ -771,8 +799,12 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
             const bool is_top = v[q] == m;
             acc[q & 3] = __fadd_rn(acc[q & 3], is_top ? 0.f : e);
             top += is_top;
-            mass += first ? 1 : fix_weight(scale, s.table, v[q]);
+            if (!have_mass) mass += first ? 1 : fix_weight(scale, s.table, v[q]);
           }
+        }
+        if (!have_mass) {
+          mass = warp_sum(mass);
+          if (lane == 0) block_mass[ch * kKeepSteps + j] = mass;
         }
       }
       float r = __fadd_rn(__fadd_rn(acc[0], acc[1]), __fadd_rn(acc[2], acc[3]));
@@ -782,15 +814,18 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
         top += __shfl_xor_sync(0xffffffffu, top, o);
       }
       st = make_float2(m, __fadd_rn(r, static_cast<float>(top - 1)));
-      mass = warp_sum(mass);
+    } else if (lane < kKeepSteps) {
+      block_mass[ch * kKeepSteps + lane] = 0;
     }
-    mass_all += mass;
-    if (lane == 0) chunk_mass[ch] = mass;
+    __syncwarp();
+    if (lane == 0)
+      for (int j = 0; j < kKeepSteps && ch * kKeepChunk + j * kBlock < n; ++j)
+        mine += block_mass[ch * kKeepSteps + j];
     if (lane < parts) cluster.map_shared_rank(states, lane)[part * a.per + ch] = st;
   }
   if (keep && threadIdx.x == 0 && v0 + n == V)  // the last word's bytes past V
     for (int b = (V + 7) / 8; b < a.words * 4; ++b) keep[b] = 0;
-  const uint64_t mine = block_sum(s, lane == 0 ? mass_all : 0);
+  mine = block_sum(s, mine);
   const int kept = static_cast<int>(block_sum(s, count));
   if (threadIdx.x < static_cast<unsigned>(parts)) {
     FilterShared* o = cluster.map_shared_rank(&s, threadIdx.x);
@@ -805,16 +840,16 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
     total += s.part_a[i];
     kept_all += s.part_n[i];
   }
-  bool exact;
-  uint64_t r = first ? 0 : mul_frac(total, u, &exact);  // the token: running sum > u * total
+  uint64_t r = first ? 0 : __umul64hi(total, frac64(u));  // the token: running sum > u * total
   if (r < before || r - before >= mine) return;  // (nobody writes to this CTA any more)
   r -= before;
 
-  // ---- the chunk, then the column
+  // ---- the block, then the column
   if (warp == 0) {
+    const int blocks = (n + kBlock - 1) / kBlock;
     uint64_t at = 0;
-    for (int c0 = 0;; c0 += 32) {
-      const uint64_t x = c0 + lane < own_chunks ? chunk_mass[c0 + lane] : 0;
+    for (int b0 = 0;; b0 += 32) {
+      const uint64_t x = b0 + lane < blocks ? block_mass[b0 + lane] : 0;
       uint64_t inc = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -822,9 +857,9 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
         if (lane >= o) inc += y;
       }
       const uint32_t b = __ballot_sync(0xffffffffu, at + inc > r);
-      if (b || c0 + 32 >= own_chunks) {
+      if (b || b0 + 32 >= blocks) {
         if (lane == (b ? __ffs(b) - 1 : 0)) {
-          s.hit = c0 + lane;
+          s.hit = b0 + lane;
           s.rest = r - (at + inc - x);
         }
         break;
@@ -833,32 +868,18 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
     }
   }
   __syncthreads();
-  const int base = s.hit * kKeepChunk;
   r = s.rest;
-  constexpr int kCols = kKeepChunk / kFilterThreads;
-  uint64_t w[kCols], sum = 0, all;
-  float x[kCols];
-#pragma unroll
-  for (int q = 0; q < kCols; ++q) {
-    const int i = base + threadIdx.x * kCols + q;
-    w[q] = 0;
-    x[q] = 0.f;
-    if (i < n) {
-      x[q] = to_f32(z[i]);
-      if (cut.has(x[q], v0 + i)) w[q] = first ? 1 : fix_weight(scale, s.table, x[q]);
-    }
-    sum += w[q];
+  const int i = s.hit * kBlock + static_cast<int>(threadIdx.x);
+  uint64_t w = 0, all;
+  float x = 0.f;
+  if (threadIdx.x < kBlock && i < n) {
+    x = to_f32(z[i]);
+    if (cut.has(x, v0 + i)) w = first ? 1 : fix_weight(scale, s.table, x);
   }
-  uint64_t at = block_scan(s.red, sum, all);
-  if (r >= at && r < at + sum) {
-#pragma unroll
-    for (int q = 0; q < kCols; ++q) {
-      if (r >= at && r < at + w[q]) {
-        a.tokens[row] = v0 + base + threadIdx.x * kCols + q;
-        s.redf[0] = x[q];
-      }
-      at += w[q];
-    }
+  const uint64_t at = block_scan(s.red, w, all);
+  if (r >= at && r - at < w) {
+    a.tokens[row] = v0 + i;
+    s.redf[0] = x;
   }
   __syncthreads();
   if (warp == 0) {
@@ -904,8 +925,7 @@ cudaError_t launch(FilterArgs a, int64_t T, cudaStream_t st) {
          parts < a.chunks)
     parts *= 2;
   a.per = per(parts);
-  const size_t fixed = ((sizeof(FilterShared) + 15) / 16 * 16 +
-                        static_cast<size_t>(a.chunks + a.per) * 8 + 127) / 128 * 128;
+  const size_t fixed = filter_fixed_bytes(a.chunks, a.per);
   if (fixed + bytes(parts) <= kSmemLimit)
     return launch_as<E, true>(a, T, parts, fixed + bytes(parts), st);
   return launch_as<E, false>(a, T, parts, fixed, st);

@@ -4,16 +4,17 @@
 // With c = log2(e) / tau (as c_hi + c_lo, both fp32) and y = (zmax - z) c >= 0:
 //   d = zmax - z rounded, e its exact rounding error  (Knuth's two-term sum)
 //   y = p + q,  p = d c_hi rounded,  q = its error + d c_lo + e c_hi
-//   p = k / 2048 + r,  k = round(2048 p),  |r + q| <= 2^-12
-//   2^-y = 2^-(k >> 11) * 2^-((k & 2047) / 2048) * 2^-(r + q)
-// the second factor from a table of 45 fractional bits, the third as 1 + g
-// with a cubic in r + q (truncated terms below 2^-53) and g rounded to 2^-34.
-// So the weight's relative error is about 2^-35, random from element to
-// element, plus the rounding to 2^-Q at the end (to nearest: a truncation
-// would take 2^-Q/2 from each of a row's many small weights, which moves the
-// running sum by a visible part of a token).  Some 30 fp32 and integer
+//   p = k / 1024 + r,  k = round(1024 p),  |r + q| <= 2^-11
+//   2^-y = 2^-(k >> 10) * 2^-((k & 1023) / 1024) * 2^-(r + q)
+// the second factor from a table of 30 fractional bits, the third as 1 + g
+// with a cubic in r + q (truncated terms below 2^-50) and g rounded to 2^-32.
+// So the weight's relative error is about 2^-32, random from element to
+// element: it moves a running sum over K tokens by 2^-32 sqrt(K) of one of
+// them.  The rounding to 2^-Q at the end is to nearest (a truncation would take
+// 2^-Q / 2 from each of a row's many small weights).  Some 30 fp32 and integer
 // instructions; the part's fp64 units (two FMAs a clock on an SM) would take
-// fifty times as long.
+// fifty times as long.  A table of 64-bit entries with 2^-45 takes twice the
+// shared-memory cycles, which bound the pass.
 #pragma once
 
 #include <cmath>
@@ -21,22 +22,22 @@
 
 namespace rz {
 
-constexpr int kFixTableBits = 11;
+constexpr int kFixTableBits = 10;
 constexpr int kFixTable = 1 << kFixTableBits;
 constexpr int kFixQ = 44;
 
 struct FixTable {
-  uint64_t v[kFixTable];
+  uint32_t v[kFixTable];
 };
 
-// 2^(-j/2048) by the exponential series, rounded to 45 fractional bits.
+// 2^(-j/1024) by the exponential series, rounded to 30 fractional bits.
 constexpr FixTable make_fix_table() {
   FixTable t{};
   for (int j = 0; j < kFixTable; ++j) {
     const double x = -0.69314718055994530942 * j / kFixTable;
     double s = 1.0;
     for (int n = 19; n >= 1; --n) s = 1.0 + x / n * s;
-    t.v[j] = static_cast<uint64_t>(s * 35184372088832.0 + 0.5);  // 2^45
+    t.v[j] = static_cast<uint32_t>(s * 1073741824.0 + 0.5);  // 2^30
   }
   return t;
 }
@@ -51,7 +52,12 @@ __host__ __device__ inline int fix_bits(int V) {
 
 struct FixScale {
   float zmax, c_hi, c_lo;
-  int drop;  // kFixQ - Q
+  float none;  // Q + 2: a larger y weighs nothing
+  int drop;    // 61 - Q
+  __host__ __device__ void bits(int q) {
+    none = static_cast<float>(q + 2);
+    drop = 61 - q;
+  }
 };
 
 __host__ __device__ __forceinline__ uint32_t fix_bits_of(float x) {
@@ -86,29 +92,29 @@ __host__ __device__ __forceinline__ float fx_mul(float a, float b) {
 }
 
 // z <= zmax finite or -inf; tab: the table (shared memory on the device).
-__host__ __device__ __forceinline__ uint64_t fix_weight(const FixScale& s, const uint64_t* tab,
+__host__ __device__ __forceinline__ uint64_t fix_weight(const FixScale& s, const uint32_t* tab,
                                                         float z) {
   const float d = fx_sub(s.zmax, z);
   const float zz = fx_sub(s.zmax, d);  // the part of z that d accounts for
   const float e = fx_add(fx_sub(s.zmax, fx_add(d, zz)), fx_sub(zz, z));
   const float p = fx_mul(d, s.c_hi);
-  if (!(p < 50.f)) return 0;           // rounds to 0 (and z = -inf)
+  if (!(p < s.none)) return 0;         // (and z = -inf)
   float q = fmaf(d, s.c_hi, -p);
   q = fmaf(d, s.c_lo, q);
   q = fmaf(e, s.c_hi, q);
-  const float big = 6144.f;            // spacing of floats there: 2^-11
+  const float big = 12288.f;           // spacing of floats there: 2^-10
   const float pk = fx_add(p, big);
   const uint32_t k = fix_bits_of(pk) - fix_bits_of(big);
   const float r = fx_add(fx_sub(p, fx_sub(pk, big)), q);
   float t = fmaf(r, -0.055504109f, 0.24022651f);  // -(ln 2)^3/6, (ln 2)^2/2
   t = fmaf(t, r, -0.69314718f);
   const float g = fx_mul(t, r);
-  const float one = 7.32421875e-4f;    // 1.5 * 2^-11: spacing 2^-34
+  const float one = 2.9296875e-3f;     // 1.5 * 2^-9: spacing 2^-32
   const int32_t gi = static_cast<int32_t>(fix_bits_of(fx_add(g, one)) - fix_bits_of(one));
-  const uint64_t w = tab[k & (kFixTable - 1)];
-  const int64_t m = static_cast<int64_t>(gi) * static_cast<int32_t>(w >> 15);  // 2^-64 units
-  const uint64_t v = w + static_cast<uint64_t>(m >> 19);
-  return ((v >> ((k >> kFixTableBits) + s.drop)) + 1) >> 1;
+  const uint32_t w = tab[k & (kFixTable - 1)];
+  const uint64_t v = (static_cast<uint64_t>(w) << 32) +
+                     static_cast<uint64_t>(static_cast<int64_t>(static_cast<int32_t>(w)) * gi);
+  return ((v >> ((k >> kFixTableBits) + s.drop)) + 1) >> 1;  // v: 62 fractional bits
 }
 
 }  // namespace rz

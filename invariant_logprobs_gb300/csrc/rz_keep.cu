@@ -57,12 +57,11 @@ struct MaskKept {
   }
 };
 
-// Whether a chunk has any kept column (warp-uniform): its 64 words at once.
+// Whether a chunk has any kept column (warp-uniform): its 32 words at once.
 __device__ __forceinline__ bool chunk_any(const uint32_t* words, int n_words, int chunk) {
   if (!words) return true;
   const int w = chunk * (kKeepChunk / 32) + (threadIdx.x & 31);
-  uint32_t x = w < n_words ? words[w] : 0u;
-  if (w + 32 < n_words) x |= words[w + 32];
+  const uint32_t x = w < n_words ? words[w] : 0u;
   return __any_sync(0xffffffffu, x != 0);
 }
 
@@ -175,7 +174,7 @@ __global__ void __launch_bounds__(kKeepThreads) keep_logprob_bwd_kernel(const Ke
   for (int ch = blockIdx.y * kKeepWarps + warp; ch < a.chunks; ch += step) {
     const bool any = g != 0.f && chunk_any(kept.words, a.words, ch);
 #pragma unroll 2
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < kKeepSteps; ++j) {
       const int col = ch * kKeepChunk + 256 * j + 8 * lane;
       if (col >= a.V) break;
       float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -205,7 +204,7 @@ cudaError_t launch_fwd(const KeepArgs& a, cudaStream_t st) {
     parts *= 2;
   const size_t smem = static_cast<size_t>(a.chunks) * sizeof(float2);
   cudaError_t e = cudaFuncSetAttribute(keep_logprob_kernel<E>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 131072);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(a.T * parts));

@@ -2,8 +2,8 @@
 // reading a row of logits of any of the three types, the row's temperature,
 // and the log-sum-exp over kept columns.
 //
-// The log-sum-exp runs over chunks of 2,048 columns.  A warp folds a chunk:
-// lane l holds columns 256 j + 8 l .. + 7 (j = 0..7) of it, takes the chunk's
+// The log-sum-exp runs over chunks of 1,024 columns.  A warp folds a chunk:
+// lane l holds columns 256 j + 8 l .. + 7 (j = 0..3) of it, takes the chunk's
 // maximum m over the kept ones and r = sum 2^((z - m) log2(e) / tau) over all of
 // them but one maximum (whose term is 1), columns not kept adding exactly 0;
 // the chunks' states are merged in a fixed order.  With that 1 left out,
@@ -25,7 +25,8 @@
 
 namespace rz {
 
-constexpr int kKeepChunk = 2048;
+constexpr int kKeepChunk = 1024;
+constexpr int kKeepSteps = kKeepChunk / 256;
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -88,10 +89,10 @@ template <class E, class Kept>
 __device__ __forceinline__ float2 keep_fold(const E* row, bool vec, int V, int chunk, float c,
                                             const Kept& kept) {
   const int col0 = chunk * kKeepChunk + 8 * (threadIdx.x & 31);
-  float v[8][8];
+  float v[kKeepSteps][8];
   float m = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < kKeepSteps; ++j) {
     const int col = col0 + 256 * j;
     uint32_t bits = col < V ? kept.before(col) : 0u;
     if (bits) {
@@ -110,7 +111,7 @@ __device__ __forceinline__ float2 keep_fold(const E* row, bool vec, int V, int c
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   int top = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+  for (int j = 0; j < kKeepSteps; ++j)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float t = ex2_approx(__fmul_rn(__fsub_rn(v[j][i], ref), c));

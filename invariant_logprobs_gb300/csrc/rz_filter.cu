@@ -16,9 +16,9 @@
 //      from the counts and the bins' edges follow the bin of the k-th logit
 //      and, as bounds on every mass, the few bins that top-p's border can be in;
 //   3  (top-p) the exact masses above and below those bins; (both) what is in
-//      them goes to a list of the first CTA, which sorts it and adds up its
-//      masses in that order (a list that overflows, as with very many equal
-//      logits: 8 bits of the key at a time over the row);
+//      them goes to a list of the first CTA, which finds the border in it by
+//      splitting its range 256 ways (a list that overflows, as with very many
+//      equal logits: 8 bits of the key at a time over the row);
 //   4  the kept set's bits, the log-sum-exp as the learner takes it and, where
 //      pass 3 has not, the mass of each 256 columns; then the 256 columns and
 //      the one of them where the running sum passes u.
@@ -41,7 +41,7 @@ constexpr int kFilterThreads = 512;
 constexpr int kFilterWarps = kFilterThreads / 32;
 constexpr int kMaxParts = 8;      // CTAs of a row
 constexpr int kBins = 2048;
-constexpr int kList = 2048;       // entries that are sorted, not searched for
+constexpr int kList = 2048;       // entries of the list
 constexpr int kBlock = 256;       // columns to a mass
 constexpr size_t kSliceMax = 81920;  // two CTAs an SM
 constexpr size_t kSmemLimit = 232448;  // of a CTA alone on its SM
@@ -113,15 +113,17 @@ struct FilterShared {
   union {
     uint32_t bins[kBins];
     uint64_t list[kList];  // (first CTA) once the bins have been read
-    struct {
-      uint32_t count[256], lo[256], hi[256];
-    } digit;            // once the list has overflowed
   };
+  struct {
+    uint32_t count[256], lo[256], hi[256];
+  } digit;
+  uint64_t few[32], range[2];
+  int n_few;
   uint64_t red[kFilterWarps];
   float redf[2 * kFilterWarps];
   // written by every CTA of the cluster
   float part_max[kMaxParts], part_min[kMaxParts];
-  int part_nan[kMaxParts], part_n[kMaxParts];
+  int part_n[kMaxParts];
   uint64_t part_a[kMaxParts], part_b[kMaxParts];
   int listed;  // (first CTA)
   // written by the first CTA
@@ -135,8 +137,55 @@ struct FilterShared {
   float c_hi, c_lo;
   double min_p_reach;
   // scratch
-  int hit, top;
+  int hit;
   uint64_t rest;
+};
+
+// Maximum, or NaN if there is one: two logits an instruction where the type has it.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+template <class E>
+struct MaxNan;
+template <>
+struct MaxNan<float> {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  __device__ __forceinline__ void add(const uint4& q) {
+    m[0] = max_nan(m[0], __uint_as_float(q.x));
+    m[1] = max_nan(m[1], __uint_as_float(q.y));
+    m[2] = max_nan(m[2], __uint_as_float(q.z));
+    m[3] = max_nan(m[3], __uint_as_float(q.w));
+  }
+  __device__ __forceinline__ float get() const {
+    return max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3]));
+  }
+};
+template <class Two>
+struct MaxNan2 {
+  Two m[4];
+  __device__ __forceinline__ void add(const uint4& q) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = __hmax2_nan(m[i], *reinterpret_cast<const Two*>(&w[i]));
+  }
+  __device__ __forceinline__ float get() const {
+    const Two t = __hmax2_nan(__hmax2_nan(m[0], m[1]), __hmax2_nan(m[2], m[3]));
+    return max_nan(to_f32(t.x), to_f32(t.y));
+  }
+};
+template <>
+struct MaxNan<__nv_bfloat16> : MaxNan2<__nv_bfloat162> {
+  __device__ __forceinline__ MaxNan() {
+    for (int i = 0; i < 4; ++i) m[i] = __float2bfloat162_rn(-INFINITY);
+  }
+};
+template <>
+struct MaxNan<__half> : MaxNan2<__half2> {
+  __device__ __forceinline__ MaxNan() {
+    for (int i = 0; i < 4; ++i) m[i] = __float2half2_rn(-INFINITY);
+  }
 };
 
 template <class Tv>
@@ -177,26 +226,6 @@ __device__ __forceinline__ Tv block_scan(Tv* scratch, Tv x, Tv& total) {
     total += v;
   }
   return base + inc - x;
-}
-
-// Descending sort of s.list[0 .. size) by the block, size a power of two of at
-// least 64: a bitonic network, a warp's pairs within the same 64 entries
-// wherever the stride allows, so that most steps need no block barrier.
-__device__ void sort_list(FilterShared& s, int size) {
-  for (int k = 2; k <= size; k <<= 1) {
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int p = threadIdx.x; p < size / 2; p += kFilterThreads) {
-        const int i = (p & ~(j - 1)) * 2 + (p & (j - 1));
-        const uint64_t x = s.list[i], y = s.list[i + j];
-        if ((x < y) == ((i & k) == 0)) {
-          s.list[i] = y;
-          s.list[i + j] = x;
-        }
-      }
-      if (j > 32 || (j == 1 && k >= 64)) __syncthreads();
-      else __syncwarp();
-    }
-  }
 }
 
 // ------------------------------------------------------------------ selection
@@ -246,6 +275,93 @@ __device__ __forceinline__ void digit_find(FilterShared& s, uint64_t target, uin
     s.digit_now = 255 - 8 * lane - i;
     s.above = a;
   }
+}
+
+// Over the list of n entries (first CTA): the smallest entry e such that those
+// above it amount to less than `target`, and that amount.  Entries are in a
+// total order, so ties need no care.  The entries' range is split 256 ways
+// until a warp can hold what is left.
+__device__ uint64_t select_list(FilterShared& s, const FixScale& scale, bool mass, int n,
+                                uint64_t target) {
+  const int lane = threadIdx.x & 31;
+  uint64_t lo = ~0ull, hi = 0;
+  for (int i = threadIdx.x; i < n; i += kFilterThreads) {
+    const uint64_t e = s.list[i];
+    lo = e < lo ? e : lo;
+    hi = e > hi ? e : hi;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const uint64_t x = __shfl_xor_sync(0xffffffffu, lo, o), y = __shfl_xor_sync(0xffffffffu, hi, o);
+    lo = x < lo ? x : lo;
+    hi = y > hi ? y : hi;
+  }
+  if (threadIdx.x == 0) {
+    s.range[0] = ~0ull;
+    s.range[1] = 0;
+  }
+  __syncthreads();
+  if (lane == 0 && lo <= hi) {
+    atomicMin(reinterpret_cast<unsigned long long*>(&s.range[0]), lo);
+    atomicMax(reinterpret_cast<unsigned long long*>(&s.range[1]), hi);
+  }
+  __syncthreads();
+  lo = s.range[0];
+  hi = s.range[1];
+  uint64_t above = 0;
+  while (true) {
+    const uint64_t width = hi - lo;
+    const int sh = width < 256 ? 0 : 56 - __clzll(width);  // width >> sh < 256
+    for (int i = threadIdx.x; i < 256; i += kFilterThreads)
+      s.digit.count[i] = s.digit.lo[i] = s.digit.hi[i] = 0;
+    if (threadIdx.x == 0) s.n_few = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kFilterThreads) {
+      const uint64_t e = s.list[i];
+      if (e < lo || e > hi) continue;
+      const uint32_t b = static_cast<uint32_t>((e - lo) >> sh);
+      digit_add(s, b, 1, false);
+      if (mass) digit_add(s, b, fix_weight(scale, s.table, entry_value(e)), true);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32)
+      digit_find(s, target, above, [&](int b) {
+        return mass ? (static_cast<uint64_t>(s.digit.hi[b]) << 32) + s.digit.lo[b]
+                    : static_cast<uint64_t>(s.digit.count[b]);
+      });
+    __syncthreads();
+    const uint32_t b = s.digit_now;
+    above = s.above;
+    const uint32_t left = s.digit.count[b];
+    lo += static_cast<uint64_t>(b) << sh;
+    hi = lo + ((1ull << sh) - 1);
+    if (left <= 32 || sh == 0) break;
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < n; i += kFilterThreads) {
+    const uint64_t e = s.list[i];
+    if (e >= lo && e <= hi) s.few[atomicAdd(&s.n_few, 1) & 31] = e;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int m = min(s.n_few, 32);
+    const uint64_t e = lane < m ? s.few[lane] : 0;
+    const uint64_t w = lane < m ? (mass ? fix_weight(scale, s.table, entry_value(e)) : 1) : 0;
+    uint64_t up = above;
+    for (int i = 0; i < m; ++i) {
+      const uint64_t o = __shfl_sync(0xffffffffu, e, i), x = __shfl_sync(0xffffffffu, w, i);
+      if (o > e) up += x;
+    }
+    uint64_t last = lane < m && up < target ? e : ~0ull;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const uint64_t x = __shfl_xor_sync(0xffffffffu, last, o);
+      last = x < last ? x : last;
+    }
+    if (lane == 0) s.rest = last;
+  }
+  __syncthreads();
+  return s.rest;
 }
 
 // Over the row: every CTA of the cluster looks through its slice z (columns
@@ -319,24 +435,26 @@ __device__ void select_row(FilterShared& s, cg::cluster_group& cluster, const Fi
 }
 
 // ------------------------------------------------------------------ bins
-// y of a logit as the weights take it (rounded: bins only need an order that
-// agrees with the logits'), and its bin.
+// The bin of a logit: y = (max - z) log2(e) / tau in equal steps, rounded in any
+// way whose order agrees with the logits'.
 struct Binning {
-  float zmax, c_hi, scale;
+  float zmax, scale;  // scale: bins for a unit of the logits
   __device__ __forceinline__ int bin(float z) const {
-    const float y = __fmul_rn(__fsub_rn(zmax, z), c_hi);
-    return static_cast<int>(fminf(__fmul_rn(y, scale), static_cast<float>(kBins - 1)));
+    // (adding 2^23 leaves the rounded integer in the float's low bits)
+    const float y = fmaf(__fsub_rn(zmax, z), scale, 8388608.f);
+    return static_cast<int>(__float_as_uint(fminf(y, 8388608.f + (kBins - 1))) & 0xfffu);
   }
-  // Bounds on the weight of what is in bin b: the table's steps of 2^-10 just
-  // outside of it (and one more for the roundings of y).  per = steps a bin.
+  // Bounds on the weight of what is in bin b, y within half a bin of it: the
+  // table's steps of 2^-10 just outside of that (and one more for the
+  // roundings of y).  per = steps a bin.
   __device__ __forceinline__ uint64_t most(const uint32_t* tab, int drop, float per, int b) const {
-    const int k = static_cast<int>(b * per) - 2;
+    const int k = static_cast<int>((b - 0.5f) * per) - 3;
     return at(tab, drop, k < 0 ? 0 : k) + 1;
   }
   __device__ __forceinline__ uint64_t least(const uint32_t* tab, int drop, float per,
                                             int b) const {
     if (b == kBins - 1) return 0;
-    return at(tab, drop, static_cast<int>((b + 1) * per) + 3);
+    return at(tab, drop, static_cast<int>((b + 0.5f) * per) + 3);
   }
   static __device__ __forceinline__ uint64_t at(const uint32_t* tab, int drop, int k) {
     const int sh = (k >> kFixTableBits) + drop;
@@ -373,13 +491,6 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
   const E* z = kResident ? slice : zrow + v0;
 
   // ---- 1: the slice, its maximum, minimum and NaNs
-  float mx = -INFINITY, mn = INFINITY;
-  bool nan = false;
-  const auto look = [&](float x) {
-    nan |= !(x == x);
-    mx = fmaxf(mx, x);
-    mn = fminf(mn, x > -INFINITY ? x : mn);
-  };
   for (int i = threadIdx.x; i < kFixTable; i += kFilterThreads) s.table[i] = g_fix_table.v[i];
   for (int i = threadIdx.x; i < kBins; i += kFilterThreads) s.bins[i] = 0;
   const float temperature = a.temperature ? a.temperature[row] : 1.f;
@@ -395,71 +506,80 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
     s.c_lo = static_cast<float>(c - static_cast<double>(s.c_hi));
     s.min_p_reach = mp > 0.f ? static_cast<double>(tau) * log(static_cast<double>(mp)) : 0.0;
   }
+  float mx = -INFINITY, mn = INFINITY;  // the maximum (NaN if there is one), a sample's minimum
   {
     const E* src = zrow + v0;
-    constexpr int kPer = 16 / sizeof(E);
+    constexpr int kPer = 16 / sizeof(E), kAhead = 8;
     const int vecs = row_aligned(src) ? n / kPer : 0;
     const uint4* src4 = reinterpret_cast<const uint4*>(src);
     uint4* dst4 = reinterpret_cast<uint4*>(slice);
-    for (int i0 = threadIdx.x; i0 < vecs; i0 += 4 * kFilterThreads) {
-      uint4 q[4];
+    MaxNan<E> top;
+    for (int i0 = threadIdx.x; i0 < vecs; i0 += kAhead * kFilterThreads) {
+      uint4 q[kAhead];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < kAhead; ++u)
         if (i0 + u * kFilterThreads < vecs) q[u] = src4[i0 + u * kFilterThreads];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kAhead; ++u) {
         const int i = i0 + u * kFilterThreads;
         if (i < vecs) {
           if (kResident) dst4[i] = q[u];
-          const E* e = reinterpret_cast<const E*>(&q[u]);
+          top.add(q[u]);
+        }
+      }
+      if (i0 == static_cast<int>(threadIdx.x)) {
+        const E* e = reinterpret_cast<const E*>(&q[0]);
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) look(to_f32(e[k]));
+        for (int k = 0; k < kPer; ++k) {
+          const float x = to_f32(e[k]);
+          mn = fminf(mn, x > -INFINITY ? x : mn);
         }
       }
     }
+    mx = top.get();
     for (int i = vecs * kPer + threadIdx.x; i < n; i += kFilterThreads) {
       const E e = src[i];
       if (kResident) slice[i] = e;
-      look(to_f32(e));
+      const float x = to_f32(e);
+      mx = max_nan(mx, x);
+      mn = fminf(mn, x > -INFINITY ? x : mn);
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
   }
   if (lane == 0) {
     s.redf[warp] = mx;
     s.redf[kFilterWarps + warp] = mn;
   }
-  const int any_nan = __syncthreads_or(nan);
+  __syncthreads();
   cluster.barrier_wait();  // every CTA runs
   if (threadIdx.x < static_cast<unsigned>(parts)) {
     mx = s.redf[0];
     mn = s.redf[kFilterWarps];
     for (int w = 1; w < kFilterWarps; ++w) {
-      mx = fmaxf(mx, s.redf[w]);
+      mx = max_nan(mx, s.redf[w]);
       mn = fminf(mn, s.redf[kFilterWarps + w]);
     }
     FilterShared* o = cluster.map_shared_rank(&s, threadIdx.x);
     o->part_max[part] = mx;
     o->part_min[part] = mn;
-    o->part_nan[part] = any_nan;
   }
   cluster.sync();
   float zmax = s.part_max[0], zmin = s.part_min[0];
-  int bad_logits = s.part_nan[0];
   for (int i = 1; i < parts; ++i) {
-    zmax = fmaxf(zmax, s.part_max[i]);
+    zmax = max_nan(zmax, s.part_max[i]);
     zmin = fminf(zmin, s.part_min[i]);
-    bad_logits |= s.part_nan[i];
   }
+  zmin = fminf(zmin, zmax);
 
   int k = a.top_k ? a.top_k[row] : 0;
   if (k <= 0 || k > V) k = V;
   if (temperature == 0.f) k = 1;
   const bool bad_param = !(tau == tau) || !(u >= 0.f && u < 1.f) || !(p == p) || !(mp <= 1.f);
-  bad_logits |= !(zmax < INFINITY && zmax > -INFINITY);
+  const bool bad_logits = !(zmax < INFINITY && zmax > -INFINITY);
   if (bad_param || bad_logits) {
     if (a.keep)
       for (int i = threadIdx.x; i < (n + 31) / 32; i += kFilterThreads)
@@ -487,11 +607,10 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
     const uint64_t pf = want_p && p > 0.f ? frac64(p) : 0;
     Binning bn;
     bn.zmax = zmax;
-    bn.c_hi = scale.c_hi;
-    // 2,048 bins over the row's range, at most 32 (in y; what is beyond weighs
-    // next to nothing) and no finer than the table
+    // 2,048 bins over the row's range, as a sample of it has it, at most 32 (in
+    // y; what is beyond weighs next to nothing) and no finer than the table
     const float range = fminf(fmaxf(__fmul_rn(__fsub_rn(zmax, zmin), scale.c_hi), 2.f), 32.f);
-    bn.scale = (kBins - 2) / range;
+    bn.scale = (kBins - 2) / range * scale.c_hi;
     for (int i = threadIdx.x; i < n; i += kFilterThreads) {
       const float x = to_f32(z[i]);
       if (x > -INFINITY) atomicAdd(&s.bins[bn.bin(x)], 1u);
@@ -587,21 +706,25 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
       if (i < n) {
         float v[8];
         load8(z, vec, n, i, v);
+        uint32_t listed = 0;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          const float x = v[q];
-          const int b = bn.bin(x);
-          if (b > bin_k || !(x > -INFINITY)) continue;
-          const bool listed = (b >= bin_lo && b <= bin_hi) || b == bin_k;
-          if (!listed && !want_p) continue;
-          if (listed) {
-            const int at = atomicAdd(&first_cta->listed, 1);
-            if (at < kList) first_cta->list[at] = entry_of(x, v0 + i + q);
-          } else {
-            const uint64_t w = fix_weight(scale, s.table, x);
-            if (b < bin_lo) mass += w;
-            else sum_r += w;
+          const int b = v[q] > -INFINITY ? bn.bin(v[q]) : kBins + 1;
+          if ((b >= bin_lo && b <= bin_hi) || b == bin_k) listed |= 1u << q;
+          if (want_p) {
+            const uint64_t w = fix_weight(scale, s.table, v[q]);
+            mass += b < bin_lo ? w : 0;
+            sum_r += b > bin_hi && b < bin_k ? w : 0;
           }
+        }
+        while (listed) {
+          const int q = __ffs(listed) - 1;
+          listed &= listed - 1;
+          float x = v[0];
+#pragma unroll
+          for (int t = 1; t < 8; ++t) x = q == t ? v[t] : x;
+          const int at = atomicAdd(&s.listed, 1);
+          if (at < kList) s.list[at] = entry_of(x, v0 + i + q);
         }
       }
       if (want_p) {
@@ -621,73 +744,54 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
         o->part_b[part] = sum_r;
       }
     }
+    if (!lead) {
+      // its entries behind those that are there (an atomic each on another
+      // CTA's memory would take longer than the pass)
+      __syncthreads();
+      const int own = s.listed;
+      if (threadIdx.x == 0) s.n_few = atomicAdd(&first_cta->listed, own);
+      __syncthreads();
+      for (int i = threadIdx.x; i < min(own, kList); i += kFilterThreads)
+        if (s.n_few + i < kList) first_cta->list[s.n_few + i] = s.list[i];
+    }
     cluster.sync();
     if (lead) {
       const int listed = s.listed;
       if (listed <= kList) {
-        int size = 64;
-        while (size < listed) size *= 2;
-        for (int i = listed + threadIdx.x; i < size; i += kFilterThreads) s.list[i] = 0;
-        __syncthreads();
-        sort_list(s, size);
-        constexpr int kEach = kList / kFilterThreads;
-        const int e0 = threadIdx.x * kEach;
-        uint64_t e[kEach], w[kEach], sum = 0, all;
-        int over = 0;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-          e[i] = e0 + i < listed ? s.list[e0 + i] : 0;
-          if (cut_k) over += e0 + i < listed && bn.bin(entry_value(e[i])) < bin_k;
-        }
-        // how many are in by the count (the list holds whole bins: those above
-        // bin_k are among above_k)
-        int in = listed;
+        uint64_t least = 0;  // the smallest entry that is in
         if (cut_k) {
-          int over_all;
-          block_scan(reinterpret_cast<int*>(s.red), over, over_all);
-          in = min(listed, static_cast<int>(k - s.above_k) + over_all);
-        }
-        if (threadIdx.x == 0) {
-          s.top = in;
-          s.cut_t = -INFINITY;  // nothing listed: no cut
-          s.cut_last = -1;
+          // (the list holds whole bins: those above bin_k are among above_k)
+          int over = 0;
+          for (int i = threadIdx.x; i < listed; i += kFilterThreads)
+            over += bn.bin(entry_value(s.list[i])) < bin_k;
+          const uint64_t over_all = block_sum(s, over);
+          least = select_list(s, scale, false, listed, k - s.above_k + over_all);
         }
         if (want_p) {
-#pragma unroll
-          for (int i = 0; i < kEach; ++i) {
-            w[i] = e0 + i < in ? fix_weight(scale, s.table, entry_value(e[i])) : 0;
-            sum += w[i];
+          uint64_t x = 0;
+          for (int i = threadIdx.x; i < listed; i += kFilterThreads) {
+            const uint64_t e = s.list[i];
+            if (e >= least) x += fix_weight(scale, s.table, entry_value(e));
           }
-          uint64_t at = block_scan(s.red, sum, all);
-          uint64_t base = 0, total = all;
+          uint64_t total = block_sum(s, x), base = 0;
           for (int i = 0; i < parts; ++i) {
             base += s.part_a[i];
             total += s.part_a[i] + s.part_b[i];
           }
-          const uint64_t target = mass_target(total, pf);
-          at += base;
-#pragma unroll
-          for (int i = 0; i < kEach; ++i) {
-            // the first that is not in, its mass above reaching the target
-            if (e0 + i < in) {
-              if (at >= target) {
-                atomicMin(&s.top, e0 + i);
-              } else {
-                const int blk = entry_index(e[i]) / kBlock, per = a.per * (kKeepChunk / kBlock);
-                atomicAdd(reinterpret_cast<unsigned long long*>(
-                              cluster.map_shared_rank(block_mass, blk / per) + blk % per),
-                          static_cast<unsigned long long>(w[i]));
-              }
-            }
-            at += w[i];
+          const uint64_t e = select_list(s, scale, true, listed, mass_target(total, pf) - base);
+          least = e > least ? e : least;
+          for (int i = threadIdx.x; i < listed; i += kFilterThreads) {
+            const uint64_t e = s.list[i];
+            if (e < least) continue;
+            const int blk = entry_index(e) / kBlock, per = a.per * (kKeepChunk / kBlock);
+            atomicAdd(reinterpret_cast<unsigned long long*>(
+                          cluster.map_shared_rank(block_mass, blk / per) + blk % per),
+                      static_cast<unsigned long long>(fix_weight(scale, s.table, entry_value(e))));
           }
         }
-        __syncthreads();
-        if (threadIdx.x == 0 && listed > 0) {
-          // the last that is in, or (none) the first listed, left out
-          const uint64_t x = s.list[s.top > 0 ? s.top - 1 : 0];
-          s.cut_t = entry_value(x);
-          s.cut_last = s.top > 0 ? entry_index(x) : -1;
+        if (threadIdx.x == 0) {
+          s.cut_t = listed > 0 ? entry_value(least) : -INFINITY;  // nothing listed: no cut
+          s.cut_last = listed > 0 ? entry_index(least) : -1;
         }
         __syncthreads();
       }
@@ -765,24 +869,29 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
       const int i = ch * kKeepChunk + 256 * j + 8 * lane;
       if (i < n) {
         float v[8];
-        load8(z, vec, n, i, v);
-        uint32_t b = 0;
+        load8(z, vec, n, i, v);  // (-inf past the end)
+        uint32_t b = 0, ties = 0;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          if (cut.has(v[q], v0 + i + q)) {  // (load8 gives -inf past the end)
-            b |= 1u << q;
-            m = fmaxf(m, v[q]);
-          }
+          b |= v[q] > cut.t ? 1u << q : 0u;
+          ties |= v[q] == cut.t ? 1u << q : 0u;
+          m = fmaxf(m, v[q]);
+        }
+        if (ties) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (((ties >> q) & 1u) && v0 + i + q <= cut.last) b |= 1u << q;
         }
         bits |= b << (8 * j);
         if (keep) keep[(v0 + i) >> 3] = static_cast<uint8_t>(b);
       }
     }
     count += __popc(bits);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float2 st = make_float2(-INFINITY, 0.f);
-    if (m > -INFINITY) {
+    if (__any_sync(0xffffffffu, bits != 0)) {
+      // what is kept is a head of the order: the chunk's maximum is
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
       int top = 0;
 #pragma unroll
@@ -794,12 +903,18 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
           load8(z, vec, n, ch * kKeepChunk + 256 * j + 8 * lane, v);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            if (!((b >> q) & 1u)) continue;
+            const bool in = (b >> q) & 1u;
             const float e = ex2_approx(__fmul_rn(__fsub_rn(v[q], m), c));
-            const bool is_top = v[q] == m;
-            acc[q & 3] = __fadd_rn(acc[q & 3], is_top ? 0.f : e);
+            const bool is_top = in && v[q] == m;
+            acc[q & 3] = __fadd_rn(acc[q & 3], in && !is_top ? e : 0.f);
             top += is_top;
-            if (!have_mass) mass += first ? 1 : fix_weight(scale, s.table, v[q]);
+          }
+          if (!have_mass) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const uint64_t w = first ? 1 : fix_weight(scale, s.table, v[q]);
+              mass += (b >> q) & 1u ? w : 0;
+            }
           }
         }
         if (!have_mass) {

@@ -98,14 +98,14 @@ __host__ __device__ __forceinline__ uint64_t fix_weight(const FixScale& s, const
   const float zz = fx_sub(s.zmax, d);  // the part of z that d accounts for
   const float e = fx_add(fx_sub(s.zmax, fx_add(d, zz)), fx_sub(zz, z));
   const float p = fx_mul(d, s.c_hi);
-  if (!(p < s.none)) return 0;         // (and z = -inf)
+  const float pc = fminf(p, s.none);   // (what is beyond, and z = -inf, weighs 0 below)
   float q = fmaf(d, s.c_hi, -p);
   q = fmaf(d, s.c_lo, q);
   q = fmaf(e, s.c_hi, q);
   const float big = 12288.f;           // spacing of floats there: 2^-10
-  const float pk = fx_add(p, big);
+  const float pk = fx_add(pc, big);
   const uint32_t k = fix_bits_of(pk) - fix_bits_of(big);
-  const float r = fx_add(fx_sub(p, fx_sub(pk, big)), q);
+  const float r = fx_add(fx_sub(pc, fx_sub(pk, big)), q);
   float t = fmaf(r, -0.055504109f, 0.24022651f);  // -(ln 2)^3/6, (ln 2)^2/2
   t = fmaf(t, r, -0.69314718f);
   const float g = fx_mul(t, r);
@@ -114,7 +114,8 @@ __host__ __device__ __forceinline__ uint64_t fix_weight(const FixScale& s, const
   const uint32_t w = tab[k & (kFixTable - 1)];
   const uint64_t v = (static_cast<uint64_t>(w) << 32) +
                      static_cast<uint64_t>(static_cast<int64_t>(static_cast<int32_t>(w)) * gi);
-  return ((v >> ((k >> kFixTableBits) + s.drop)) + 1) >> 1;  // v: 62 fractional bits
+  const uint64_t w1 = ((v >> ((k >> kFixTableBits) + s.drop)) + 1) >> 1;  // v: 62 fractional bits
+  return p < s.none ? w1 : 0;  // (no branch: a lane's weights are evaluated side by side)
 }
 
 }  // namespace rz

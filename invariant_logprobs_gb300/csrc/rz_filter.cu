@@ -12,7 +12,7 @@
 // A row is read from memory once: a cluster of up to eight CTAs holds it in
 // shared memory, a slice of whole 1,024-column chunks each, and passes over it
 //   1  while it arrives: its maximum and minimum;
-//   2  (top-k, top-p) counts in 2,048 bins linear in y = (max - z) log2(e) / tau;
+//   2  (top-k, top-p) counts in 2,048 bins equal in y = (max - z) log2(e) / tau;
 //      from the counts and the bins' edges follow the bin of the k-th logit
 //      and, as bounds on every mass, the few bins that top-p's border can be in;
 //   3  (top-p) the exact masses above and below those bins; (both) what is in
@@ -26,6 +26,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "rz.h"
 #include "rz_fixexp.cuh"
@@ -435,32 +436,98 @@ __device__ void select_row(FilterShared& s, cg::cluster_group& cluster, const Fi
 }
 
 // ------------------------------------------------------------------ bins
-// The bin of a logit: y = (max - z) log2(e) / tau in equal steps, rounded in any
-// way whose order agrees with the logits'.
+// Bins of a row: 2^sh of the weights' steps of 2^-10 in y each, the last one
+// open.  Their order agrees with the logits'.
 struct Binning {
-  float zmax, scale;  // scale: bins for a unit of the logits
-  __device__ __forceinline__ int bin(float z) const {
-    // (adding 2^23 leaves the rounded integer in the float's low bits)
-    const float y = fmaf(__fsub_rn(zmax, z), scale, 8388608.f);
-    return static_cast<int>(__float_as_uint(fminf(y, 8388608.f + (kBins - 1))) & 0xfffu);
+  int sh;
+  __device__ __forceinline__ int bin(uint32_t k) const {
+    return static_cast<int>(min(k >> sh, static_cast<uint32_t>(kBins - 1)));
   }
-  // Bounds on the weight of what is in bin b, y within half a bin of it: the
-  // table's steps of 2^-10 just outside of that (and one more for the
-  // roundings of y).  per = steps a bin.
-  __device__ __forceinline__ uint64_t most(const uint32_t* tab, int drop, float per, int b) const {
-    const int k = static_cast<int>((b - 0.5f) * per) - 3;
-    return at(tab, drop, k < 0 ? 0 : k) + 1;
+  __device__ __forceinline__ int bin(const FixScale& s, float z) const {
+    float r;
+    return bin(s.big ? fix_steps<true>(s, z, r) : fix_steps<false>(s, z, r));
   }
-  __device__ __forceinline__ uint64_t least(const uint32_t* tab, int drop, float per,
-                                            int b) const {
-    if (b == kBins - 1) return 0;
-    return at(tab, drop, static_cast<int>((b + 0.5f) * per) + 3);
+  // Bounds on the weight of what is in bin b (y within a step of its k).
+  __device__ __forceinline__ uint64_t most(const uint32_t* tab, int drop, int b) const {
+    return at(tab, drop, max((b << sh) - 2, 0)) + 1;
+  }
+  __device__ __forceinline__ uint64_t least(const uint32_t* tab, int drop, int b) const {
+    return b == kBins - 1 ? 0 : at(tab, drop, ((b + 1) << sh) + 1);
   }
   static __device__ __forceinline__ uint64_t at(const uint32_t* tab, int drop, int k) {
-    const int sh = (k >> kFixTableBits) + drop;
-    return sh > 62 ? 0 : ((static_cast<uint64_t>(tab[k & (kFixTable - 1)]) << 32) >> sh) >> 1;
+    const int n = (k >> kFixTableBits) + drop;
+    return n > 62 ? 0 : ((static_cast<uint64_t>(tab[k & (kFixTable - 1)]) << 32) >> n) >> 1;
   }
 };
+
+// Pass 2: counts of the slice's logits by bin.
+template <bool kBig, class E>
+__device__ __forceinline__ void count_bins(FilterShared& s, const FixScale& scale,
+                                           const Binning& bn, const E* z, bool vec, int n) {
+  for (int i = 8 * threadIdx.x; i < n; i += 8 * kFilterThreads) {
+    float v[8], r;
+    load8(z, vec, n, i, v);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int b = bn.bin(fix_steps<kBig>(scale, v[q], r));
+      if (v[q] > -INFINITY) atomicAdd(&s.bins[b], 1u);
+    }
+  }
+}
+
+// Pass 3: (kMass) exact masses by blocks of what lies in bins below bin_lo, and
+// of what lies between bin_hi and bin_k; what is in bin_lo .. bin_hi and bin_k
+// is listed.  Returns (lane 0: of its warp's blocks; all lanes: of their columns).
+template <bool kBig, bool kMass, class E>
+__device__ __forceinline__ void sum_masses(FilterShared& s, const FixScale& scale,
+                                           const Binning& bn, const E* z, bool vec, int v0, int n,
+                                           int bin_k, int bin_lo, int bin_hi,
+                                           uint64_t* block_mass, uint64_t& sum_a,
+                                           uint64_t& sum_r) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t band = static_cast<uint32_t>(bin_hi - bin_lo);  // (empty: bin_hi < bin_lo)
+  const bool any_band = bin_hi >= bin_lo;
+  for (int blk = threadIdx.x >> 5; blk * kBlock < n; blk += kFilterWarps) {
+    const int i = blk * kBlock + 8 * lane;
+    uint64_t above = 0, all = 0;  // all: of top-k's head but what is listed
+    if (i < n) {
+      float v[8];
+      load8(z, vec, n, i, v);
+      uint32_t listed = 0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        float r;
+        const uint32_t steps = fix_steps<kBig>(scale, v[q], r);
+        const int b = bn.bin(steps);
+        const bool in_list = (any_band && static_cast<uint32_t>(b - bin_lo) <= band) || b == bin_k;
+        listed |= in_list ? 1u << q : 0u;
+        if (kMass) {
+          const uint64_t w = fix_weight_at(scale, s.table, steps, r);
+          if (b < bin_lo) above += w;
+          if (!in_list && b < bin_k) all += w;
+        }
+      }
+      while (listed) {
+        const int q = __ffs(listed) - 1;
+        listed &= listed - 1;
+        float x = v[0];
+#pragma unroll
+        for (int t = 1; t < 8; ++t) x = q == t ? v[t] : x;
+        if (!(x > -INFINITY)) continue;
+        const int at = atomicAdd(&s.listed, 1);
+        if (at < kList) s.list[at] = entry_of(x, v0 + i + q);
+      }
+    }
+    if (kMass) {
+      sum_r += all - above;
+      above = warp_sum(above);
+      if (lane == 0) {
+        block_mass[blk] = above;
+        sum_a += above;
+      }
+    }
+  }
+}
 
 // Shared memory ahead of the slice: FilterShared, the chunks' states, the own
 // columns' masses.
@@ -594,10 +661,7 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
     return;  // the whole cluster does; nobody's memory is in use
   }
   FixScale scale;
-  scale.zmax = zmax;
-  scale.c_hi = s.c_hi;
-  scale.c_lo = s.c_lo;
-  scale.bits(a.fix_bits);
+  scale.init(zmax, s.c_hi, s.c_lo, a.fix_bits);
 
   // ---- 2, 3: the cut
   Cut cut{-INFINITY, -1};
@@ -605,16 +669,17 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
   const bool want_k = k < V, want_p = p < 1.f;
   if (want_k || want_p) {
     const uint64_t pf = want_p && p > 0.f ? frac64(p) : 0;
+    // 2,048 bins over the row's range, as a sample of it has it
     Binning bn;
-    bn.zmax = zmax;
-    // 2,048 bins over the row's range, as a sample of it has it, at most 32 (in
-    // y; what is beyond weighs next to nothing) and no finer than the table
-    const float range = fminf(fmaxf(__fmul_rn(__fsub_rn(zmax, zmin), scale.c_hi), 2.f), 32.f);
-    bn.scale = (kBins - 2) / range * scale.c_hi;
-    for (int i = threadIdx.x; i < n; i += kFilterThreads) {
-      const float x = to_f32(z[i]);
-      if (x > -INFINITY) atomicAdd(&s.bins[bn.bin(x)], 1u);
+    {
+      float r;
+      const uint32_t most =
+          scale.big ? fix_steps<true>(scale, zmin, r) : fix_steps<false>(scale, zmin, r);
+      bn.sh = most < kBins ? 0 : 21 - __clz(most);  // most >> sh < 2,048
     }
+    const bool vec = kResident || row_aligned(z);
+    if (scale.big) count_bins<true>(s, scale, bn, z, vec, n);
+    else count_bins<false>(s, scale, bn, z, vec, n);
     __syncthreads();
     if (parts > 1) {
       if (!lead) {
@@ -652,15 +717,14 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
       if (want_p) {
         // bounds on the masses of the bins, in top-k's head
         const int bin_k = s.bin_k;
-        const float per = range * (static_cast<float>(kFixTable) / (kBins - 2));
         uint64_t lo[kEach], hi[kEach], lo_sum = 0, hi_sum = 0, lo_all, hi_all;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
           const int b = b0 + i;
           const uint32_t m = b < bin_k ? c[i] : (b == bin_k ? k - s.above_k : 0u);
           c[i] = m;
-          lo[i] = m ? m * bn.least(s.table, scale.drop, per, b) : 0;
-          hi[i] = m ? m * bn.most(s.table, scale.drop, per, b) : 0;
+          lo[i] = m ? m * bn.least(s.table, scale.drop, b) : 0;
+          hi[i] = m ? m * bn.most(s.table, scale.drop, b) : 0;
           lo_sum += lo[i];
           hi_sum += hi[i];
         }
@@ -698,43 +762,16 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
     // the exact masses above the band, by blocks, and of the rest of top-k's
     // head but the band and bin_k; what is in these two is listed
     FilterShared* first_cta = cluster.map_shared_rank(&s, 0);
-    const bool vec = kResident || row_aligned(z);
     uint64_t sum_a = 0, sum_r = 0;
-    for (int blk = warp; blk * kBlock < n; blk += kFilterWarps) {
-      const int i = blk * kBlock + 8 * lane;
-      uint64_t mass = 0;
-      if (i < n) {
-        float v[8];
-        load8(z, vec, n, i, v);
-        uint32_t listed = 0;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int b = v[q] > -INFINITY ? bn.bin(v[q]) : kBins + 1;
-          if ((b >= bin_lo && b <= bin_hi) || b == bin_k) listed |= 1u << q;
-          if (want_p) {
-            const uint64_t w = fix_weight(scale, s.table, v[q]);
-            mass += b < bin_lo ? w : 0;
-            sum_r += b > bin_hi && b < bin_k ? w : 0;
-          }
-        }
-        while (listed) {
-          const int q = __ffs(listed) - 1;
-          listed &= listed - 1;
-          float x = v[0];
-#pragma unroll
-          for (int t = 1; t < 8; ++t) x = q == t ? v[t] : x;
-          const int at = atomicAdd(&s.listed, 1);
-          if (at < kList) s.list[at] = entry_of(x, v0 + i + q);
-        }
-      }
-      if (want_p) {
-        mass = warp_sum(mass);
-        if (lane == 0) {
-          block_mass[blk] = mass;
-          sum_a += mass;
-        }
-      }
-    }
+    // (the bins are those of pass 2: the same steps)
+    const auto masses = [&](auto big, auto mass) {
+      sum_masses<decltype(big)::value, decltype(mass)::value>(
+          s, scale, bn, z, vec, v0, n, bin_k, bin_lo, bin_hi, block_mass, sum_a, sum_r);
+    };
+    using Yes = std::integral_constant<bool, true>;
+    using No = std::integral_constant<bool, false>;
+    if (scale.big) want_p ? masses(Yes(), Yes()) : masses(Yes(), No());
+    else want_p ? masses(No(), Yes()) : masses(No(), No());
     if (want_p) {
       sum_a = block_sum(s, sum_a);
       sum_r = block_sum(s, sum_r);
@@ -763,7 +800,7 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
           // (the list holds whole bins: those above bin_k are among above_k)
           int over = 0;
           for (int i = threadIdx.x; i < listed; i += kFilterThreads)
-            over += bn.bin(entry_value(s.list[i])) < bin_k;
+            over += bn.bin(scale, entry_value(s.list[i])) < bin_k;
           const uint64_t over_all = block_sum(s, over);
           least = select_list(s, scale, false, listed, k - s.above_k + over_all);
         }
@@ -870,17 +907,19 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
       if (i < n) {
         float v[8];
         load8(z, vec, n, i, v);  // (-inf past the end)
-        uint32_t b = 0, ties = 0;
+        uint32_t b = 0;
+        bool tie = false;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          b |= v[q] > cut.t ? 1u << q : 0u;
-          ties |= v[q] == cut.t ? 1u << q : 0u;
+        for (int q = 7; q >= 0; --q) {
+          // the sign of t - z, shifted in
+          b = __funnelshift_l(__float_as_uint(__fsub_rn(cut.t, v[q])), b, 1);
+          tie |= v[q] == cut.t;
           m = fmaxf(m, v[q]);
         }
-        if (ties) {
+        if (tie) {
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            if (((ties >> q) & 1u) && v0 + i + q <= cut.last) b |= 1u << q;
+            if (v[q] == cut.t && v0 + i + q <= cut.last) b |= 1u << q;
         }
         bits |= b << (8 * j);
         if (keep) keep[(v0 + i) >> 3] = static_cast<uint8_t>(b);
@@ -910,10 +949,24 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
             top += is_top;
           }
           if (!have_mass) {
+            if (first) {
+              mass = __popc(b);
+            } else if (!scale.big) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const uint64_t w = first ? 1 : fix_weight(scale, s.table, v[q]);
-              mass += (b >> q) & 1u ? w : 0;
+              for (int q = 0; q < 8; ++q) {
+                float r;
+                const uint32_t steps = fix_steps<false>(scale, v[q], r);
+                const uint64_t w = fix_weight_at(scale, s.table, steps, r);
+                if ((b >> q) & 1u) mass += w;
+              }
+            } else {
+#pragma unroll 1
+              for (int q = 0; q < 8; ++q) {
+                float x = v[0];
+#pragma unroll
+                for (int t = 1; t < 8; ++t) x = q == t ? v[t] : x;
+                if ((b >> q) & 1u) mass += fix_weight(scale, s.table, x);
+              }
             }
           }
         }

@@ -25,6 +25,8 @@ namespace cg = cooperative_groups;
 constexpr int kKeepThreads = 256;
 constexpr int kKeepWarps = kKeepThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kMaskAhead = 4;
+constexpr int kFwdCtas = 4, kBwdCtas = 32;  // CTAs wanted for each SM
 
 struct KeepArgs {
   const void* logits;
@@ -41,33 +43,34 @@ struct KeepArgs {
   int V, words, chunks;
 };
 
-struct MaskKept {
-  const uint32_t* words;  // of the row; null: all
-  int V;
-  __device__ __forceinline__ uint32_t before(int col) const {
-    const uint32_t in = V - col >= 8 ? 0xffu : (1u << (V - col)) - 1u;
-    return words ? reinterpret_cast<const uint8_t*>(words)[col >> 3] & in : in;
+// A lane's word of a chunk's mask (columns 32 l .. + 31 of it); all ones with no
+// mask; nothing past V.
+__device__ __forceinline__ uint32_t mask_word(const uint32_t* words, int V, int chunk) {
+  const int col = chunk * kKeepChunk + 32 * (threadIdx.x & 31);
+  if (col >= V) return 0u;
+  const uint32_t in = V - col >= 32 ? 0xffffffffu : (1u << (V - col)) - 1u;
+  return words ? words[col >> 5] & in : in;
+}
+// The bits of the lane's columns 256 j + 8 l .. + 7, 8 for each step j, from the
+// warp's words.
+__device__ __forceinline__ uint32_t lane_bits(uint32_t word) {
+  const int lane = threadIdx.x & 31;
+  uint32_t bits = 0;
+#pragma unroll
+  for (int j = 0; j < kKeepSteps; ++j) {
+    const uint32_t w = __shfl_sync(0xffffffffu, word, 8 * j + (lane >> 2));
+    bits |= ((w >> (8 * (lane & 3))) & 255u) << (8 * j);
   }
-  template <class A>
-  __device__ __forceinline__ uint32_t after(int, const A&, uint32_t bits) const {
-    return bits;
-  }
-  __device__ __forceinline__ bool has(int v) const {
-    return !words || ((words[v >> 5] >> (v & 31)) & 1u);
-  }
-};
-
-// Whether a chunk has any kept column (warp-uniform): its 32 words at once.
-__device__ __forceinline__ bool chunk_any(const uint32_t* words, int n_words, int chunk) {
-  if (!words) return true;
-  const int w = chunk * (kKeepChunk / 32) + (threadIdx.x & 31);
-  const uint32_t x = w < n_words ? words[w] : 0u;
-  return __any_sync(0xffffffffu, x != 0);
+  return bits;
+}
+__device__ __forceinline__ bool mask_has(const uint32_t* words, int v) {
+  return !words || ((words[v >> 5] >> (v & 31)) & 1u);
 }
 
 template <class E>
-__global__ void __launch_bounds__(kKeepThreads, 2) keep_logprob_kernel(const KeepArgs a) {
-  extern __shared__ float2 states[];  // of the whole row, in the first CTA of the cluster
+__global__ void __launch_bounds__(kKeepThreads, 4) keep_logprob_kernel(const KeepArgs a) {
+  extern __shared__ float2 states[];  // of the whole row, in the first CTA of the cluster; a list
+  __shared__ int n_list;
   cg::cluster_group cluster = cg::this_cluster();
   const int parts = static_cast<int>(cluster.num_blocks());
   const int part = static_cast<int>(cluster.block_rank());
@@ -75,14 +78,43 @@ __global__ void __launch_bounds__(kKeepThreads, 2) keep_logprob_kernel(const Kee
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const E* z = static_cast<const E*>(a.logits) + row * a.ld;
   const bool vec = row_aligned(z);
-  const MaskKept kept{a.keep ? a.keep + row * a.words : nullptr, a.V};
+  const uint32_t* mask = a.keep ? a.keep + row * a.words : nullptr;
   const float tau = row_tau(a.temperature, row);
   const float c = keep_scale(tau);
   float2* dst = cluster.map_shared_rank(states, 0);
   if (parts > 1) cluster.sync();  // every CTA of the cluster runs before its memory is written
-  for (int ch = part * kKeepWarps + warp; ch < a.chunks; ch += parts * kKeepWarps) {
-    float2 st = make_float2(-INFINITY, 0.f);
-    if (chunk_any(kept.words, a.words, ch)) st = keep_fold(z, vec, a.V, ch, c, kept);
+  // The chunks with something kept, from the mask, several loads of it under
+  // way together; most of a filtered row's hold nothing, and are done.
+  uint16_t* list = reinterpret_cast<uint16_t*>(states + a.chunks);
+  const int step = parts * kKeepWarps;
+  if (mask) {
+    if (threadIdx.x == 0) n_list = 0;
+    __syncthreads();
+    for (int ch0 = part * kKeepWarps + warp; ch0 < a.chunks; ch0 += kMaskAhead * step) {
+      uint32_t words[kMaskAhead];
+#pragma unroll
+      for (int i = 0; i < kMaskAhead; ++i) words[i] = mask_word(mask, a.V, ch0 + i * step);
+#pragma unroll
+      for (int i = 0; i < kMaskAhead; ++i) {
+        const int ch = ch0 + i * step;
+        const bool any = __any_sync(0xffffffffu, words[i] != 0);
+        if (lane == 0 && ch < a.chunks) {
+          if (any) list[atomicAdd(&n_list, 1)] = static_cast<uint16_t>(ch);
+          else dst[ch] = make_float2(-INFINITY, 0.f);
+        }
+      }
+    }
+    __syncthreads();
+  }
+  const int n = mask ? n_list : (a.chunks - part * kKeepWarps + step - 1) / step * kKeepWarps;
+#pragma unroll 1
+  for (int i = warp; i < n; i += kKeepWarps) {
+    const int ch = mask ? list[i] : part * kKeepWarps + i % kKeepWarps + i / kKeepWarps * step;
+    if (ch >= a.chunks) break;
+    const uint32_t bits = lane_bits(mask_word(mask, a.V, ch));
+    const float2 st = __any_sync(0xffffffffu, __popc(bits) > kKeepFew)
+                          ? keep_fold(z, vec, a.V, ch, c, bits)
+                          : keep_fold_few(z, ch, c, bits);
     if (lane == 0) dst[ch] = st;
   }
   if (parts > 1) cluster.sync();
@@ -95,7 +127,7 @@ __global__ void __launch_bounds__(kKeepThreads, 2) keep_logprob_kernel(const Kee
     if (t < 0 || t >= a.V) {
       lp = __int_as_float(0x7fc00000);
       if (a.err) atomicOr(a.err, RZ_DEVERR_TOKEN_RANGE);
-    } else if (!kept.has(t)) {
+    } else if (!mask_has(mask, t)) {
       lp = -INFINITY;
     } else {
       const float za = to_f32(z[t]);
@@ -149,20 +181,21 @@ __device__ __forceinline__ void store8(E* row, bool vec, int V, int col, const f
 
 template <class E>
 __global__ void __launch_bounds__(kKeepThreads) keep_logprob_bwd_kernel(const KeepArgs a) {
-  const long long row = blockIdx.x;
+  // last row first: the forward pass before has left the last rows in the L2
+  const long long row = a.T - 1 - blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // not restrict: dlogits may be the logits; every lane loads its columns
   // before it stores them, and no other lane reads them
   const E* z = static_cast<const E*>(a.logits) + row * a.ld;
   E* out = static_cast<E*>(a.dlogits) + row * a.ldd;
   const bool vec = row_aligned(z), vec_out = row_aligned(out);
-  const MaskKept kept{a.keep ? a.keep + row * a.words : nullptr, a.V};
+  const uint32_t* mask = a.keep ? a.keep + row * a.words : nullptr;
   const float tau = row_tau(a.temperature, row);
   const float lse = a.lse_in[row];
   const int t = a.tokens[row];
   const bool in = t >= 0 && t < a.V;
   float g = a.dlogprob[row];
-  if (!in || !kept.has(t) || !isfinite(lse) || !(tau == tau)) g = 0.f;
+  if (!in || !mask_has(mask, t) || !isfinite(lse) || !(tau == tau)) g = 0.f;
   if (a.err && blockIdx.y == 0 && threadIdx.x == 0) {
     if (!in) atomicOr(a.err, RZ_DEVERR_TOKEN_RANGE);
     if (!(tau == tau)) atomicOr(a.err, RZ_DEVERR_PARAM);
@@ -172,13 +205,14 @@ __global__ void __launch_bounds__(kKeepThreads) keep_logprob_bwd_kernel(const Ke
   const float gt = g / tau;
   const int step = kKeepWarps * gridDim.y;
   for (int ch = blockIdx.y * kKeepWarps + warp; ch < a.chunks; ch += step) {
-    const bool any = g != 0.f && chunk_any(kept.words, a.words, ch);
+    const uint32_t word = g != 0.f ? mask_word(mask, a.V, ch) : 0u;
+    const uint32_t all = __any_sync(0xffffffffu, word != 0) ? lane_bits(word) : 0u;
 #pragma unroll 2
     for (int j = 0; j < kKeepSteps; ++j) {
       const int col = ch * kKeepChunk + 256 * j + 8 * lane;
       if (col >= a.V) break;
       float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      const uint32_t bits = any ? kept.before(col) : 0u;
+      const uint32_t bits = (all >> (8 * j)) & 255u;
       if (bits) {
         float v[8];
         load8(z, vec, a.V, col, v);
@@ -200,11 +234,12 @@ cudaError_t launch_fwd(const KeepArgs& a, cudaStream_t st) {
   // One row to a CTA while that fills the GPU twice; else its chunks over a
   // cluster of up to eight CTAs, whose states meet in the first one's memory.
   int parts = 1;
-  while (parts < kMaxCluster && a.T * parts < 2 * num_sms() && parts * kKeepWarps < a.chunks)
+  while (parts < kMaxCluster && a.T * parts < kFwdCtas * num_sms() &&
+         parts * kKeepWarps < a.chunks)
     parts *= 2;
-  const size_t smem = static_cast<size_t>(a.chunks) * sizeof(float2);
+  const size_t smem = static_cast<size_t>(a.chunks) * (sizeof(float2) + sizeof(uint16_t));
   cudaError_t e = cudaFuncSetAttribute(keep_logprob_kernel<E>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 131072);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 196608);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(a.T * parts));
@@ -224,7 +259,8 @@ cudaError_t launch_fwd(const KeepArgs& a, cudaStream_t st) {
 template <class E>
 cudaError_t launch_bwd(const KeepArgs& a, cudaStream_t st) {
   int parts = 1;
-  while (parts < 64 && a.T * parts < 4 * num_sms() && parts * kKeepWarps < a.chunks) parts *= 2;
+  while (parts < 64 && a.T * parts < kBwdCtas * num_sms() && parts * kKeepWarps < a.chunks)
+    parts *= 2;
   keep_logprob_bwd_kernel<E><<<dim3(static_cast<unsigned>(a.T), parts), kKeepThreads, 0, st>>>(a);
   return cudaGetLastError();
 }

@@ -83,28 +83,26 @@ __device__ __forceinline__ float row_tau(const float* temperature, long long row
   return t >= 9.5367431640625e-07f && t <= 1048576.f ? t : __int_as_float(0x7fc00000);
 }
 
-// Fold of one chunk by one warp.  Kept: before(col) -> the 8 columns' bits that
-// may be kept (0: nothing is loaded), after(col, v, bits) -> those that are.
-template <class E, class Kept>
+// Fold of one chunk by one warp; bits: which of the lane's columns are kept, 8
+// for each step (none kept in a step: nothing of it is loaded).
+template <class E>
 __device__ __forceinline__ float2 keep_fold(const E* row, bool vec, int V, int chunk, float c,
-                                            const Kept& kept) {
+                                            uint32_t bits) {
   const int col0 = chunk * kKeepChunk + 8 * (threadIdx.x & 31);
   float v[kKeepSteps][8];
   float m = -INFINITY;
 #pragma unroll
   for (int j = 0; j < kKeepSteps; ++j) {
-    const int col = col0 + 256 * j;
-    uint32_t bits = col < V ? kept.before(col) : 0u;
-    if (bits) {
-      load8(row, vec, V, col, v[j]);
-      bits = kept.after(col, v[j], bits);
-    }
+    const uint32_t b = (bits >> (8 * j)) & 255u;
+    if (b) load8(row, vec, V, col0 + 256 * j, v[j]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (!((bits >> i) & 1u)) v[j][i] = -INFINITY;
-      m = fmaxf(m, v[j][i]);
-    }
+    for (int i = 0; i < 8; ++i)
+      if (!((b >> i) & 1u)) v[j][i] = -INFINITY;
   }
+#pragma unroll
+  for (int j = 0; j < kKeepSteps; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, v[j][i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float ref = m == -INFINITY ? 0.f : m;
@@ -126,6 +124,48 @@ __device__ __forceinline__ float2 keep_fold(const E* row, bool vec, int V, int c
     top += __shfl_xor_sync(0xffffffffu, top, o);
   }
   // an empty chunk: 0 (NaN if it holds NaNs)
+  return make_float2(m, m == -INFINITY ? r : __fadd_rn(r, static_cast<float>(top - 1)));
+}
+
+// The same for a chunk of which no lane keeps more than kKeepFew columns: those
+// alone, in the same order into the same sums (what keep_fold adds besides is
+// exactly 0).
+constexpr int kKeepFew = 3;
+template <class E>
+__device__ __forceinline__ float2 keep_fold_few(const E* row, int chunk, float c, uint32_t bits) {
+  const E* p = row + static_cast<long long>(chunk) * kKeepChunk + 8 * (threadIdx.x & 31);
+  float v[kKeepFew];
+  int at[kKeepFew];
+  float m = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kKeepFew; ++k) {
+    at[k] = __ffs(bits) - 1;  // 8 j + i
+    bits &= bits - 1;
+    v[k] = -INFINITY;
+    if (at[k] >= 0) v[k] = to_f32(p[32 * (at[k] & 24) + (at[k] & 7)]);
+  }
+#pragma unroll
+  for (int k = 0; k < kKeepFew; ++k) m = fmaxf(m, v[k]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float ref = m == -INFINITY ? 0.f : m;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  int top = 0;
+#pragma unroll
+  for (int k = 0; k < kKeepFew; ++k) {
+    const float t = ex2_approx(__fmul_rn(__fsub_rn(v[k], ref), c));
+    const bool is_top = v[k] == m;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      acc[q] = __fadd_rn(acc[q], !is_top && (at[k] & 3) == q ? t : 0.f);
+    top += is_top;
+  }
+  float r = __fadd_rn(__fadd_rn(acc[0], acc[1]), __fadd_rn(acc[2], acc[3]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, o));
+    top += __shfl_xor_sync(0xffffffffu, top, o);
+  }
   return make_float2(m, m == -INFINITY ? r : __fadd_rn(r, static_cast<float>(top - 1)));
 }
 

@@ -52,11 +52,14 @@ RZ_OP_LOSS_FWD_BWD_REF = 6
 RZ_OP_GROUP_DECODE_ATTN = 7
 
 _lib = None
+_torch_module = None
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+_I64x2 = _I64 * 2
+_I64x6 = _I64 * 6
 
 _SIGNATURES = {
     "rz_workspace_size": (_SZ, [ctypes.c_int, _I64, _I32, _I32, _I32]),
@@ -133,12 +136,15 @@ def workspace_size(op, T, d, V, B):
 
 # ----------------------------------------------------------------- helpers
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
@@ -147,12 +153,15 @@ def _stream(stream):
     current device's current stream."""
     torch = _torch()
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        try:  # the handle alone: the stream object takes longer than a small launch
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:
+            return torch.cuda.current_stream().cuda_stream
     dev = getattr(stream, "device", None)
     if dev is not None and dev.index is not None and dev.index != torch.cuda.current_device():
         raise ValueError("stream is on %s but the current device is cuda:%d"
                          % (dev, torch.cuda.current_device()))
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _check(name, status):
@@ -187,18 +196,24 @@ def _ws_bytes(ws):
 
 
 def _shape(t, shape, name):
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != tuple(shape):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
 def _same_device(*ts):
     """All tensors on one CUDA device, and that the current device: the
     library launches on the current device's context."""
-    devs = {t.device for t in ts if t is not None}
-    if len(devs) > 1:
-        raise ValueError("all tensors must be on one CUDA device, got %s" % sorted(map(str, devs)))
-    if devs:
-        dev = next(iter(devs))
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        d = t.device
+        if dev is None:
+            dev = d
+        elif d != dev:
+            devs = {str(x.device) for x in ts if x is not None}
+            raise ValueError("all tensors must be on one CUDA device, got %s" % sorted(devs))
+    if dev is not None:
         cur = _torch().cuda.current_device()
         if dev.type == "cuda" and dev.index is not None and dev.index != cur:
             raise ValueError("tensors are on %s but the current device is cuda:%d; call under "
@@ -737,22 +752,23 @@ def rz_group_decode_attn(q, k_cache, v_cache, table, lens, prefix_table=None, pr
     torch = _torch()
     lib = load()
     dt = _dtype_id(q, "q", (RZ_DTYPE_BF16, RZ_DTYPE_F16))
+    if q.dim() != 3:
+        raise ValueError("q must have shape [B, Hq, D], got %s" % (tuple(q.shape),))
+    B, Hq, D = q.shape
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         _dtype_id(t, name, (dt,))
         if t.dim() != 4 or t.shape[1] < 1:
             raise ValueError("%s must have shape [n_pages, page, Hkv, D], got %s"
                              % (name, tuple(t.shape)))
-    if q.dim() != 3:
-        raise ValueError("q must have shape [B, Hq, D], got %s" % (tuple(q.shape),))
-    B, Hq, D = q.shape
     n_pages, page, Hkv, _ = k_cache.shape
     _shape(k_cache, (n_pages, page, Hkv, D), "k_cache")
     _shape(v_cache, (n_pages, page, Hkv, D), "v_cache")
-    for t, name in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.stride(-1) != 1 and D > 1:
+    qst, kst, vst = q.stride(), k_cache.stride(), v_cache.stride()
+    for st, name in ((qst, "q"), (kst, "k_cache"), (vst, "v_cache")):
+        if st[-1] != 1 and D > 1:
             raise ValueError("%s must be contiguous along the head size, got strides %s"
-                             % (name, t.stride()))
-        if any(x < 0 for x in t.stride()):
+                             % (name, st))
+        if min(st) < 0:
             raise ValueError("%s has a negative stride" % name)
     _need(table, torch.int32, "table")
     _need(lens, torch.int32, "lens")
@@ -789,9 +805,9 @@ def rz_group_decode_attn(q, k_cache, v_cache, table, lens, prefix_table=None, pr
     if lse_out is None:
         lse_out = _new((B, Hq), torch.float32, q.device, stream)
     # strides of axes that hold one element mean nothing: give them as 0
-    step = lambda t, i: t.stride(i) if t.shape[i] > 1 else 0  # noqa: E731
-    qs = (ctypes.c_int64 * 2)(step(q, 0), step(q, 1))
-    kvs = (ctypes.c_int64 * 6)(*[step(t, i) for t in (k_cache, v_cache) for i in range(3)])
+    qs = _I64x2(qst[0] if B > 1 else 0, qst[1] if Hq > 1 else 0)
+    many = (n_pages > 1, page > 1, Hkv > 1)
+    kvs = _I64x6(*[st[i] if many[i] else 0 for st in (kst, vst) for i in range(3)])
     st = lib.rz_group_decode_attn(_ptr(q), qs, _ptr(k_cache), _ptr(v_cache), kvs, n_pages, page,
                                   _ptr(prefix_table), prefix_width, _ptr(prefix_lens),
                                   _ptr(cu_group), P, _ptr(table), table.shape[1], _ptr(lens), B,

@@ -7,6 +7,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -18,21 +19,41 @@
 namespace rz {
 
 // ------------------------------------------------------------------ device facts
+namespace {
+// SM count and compute capability of a device, looked up once (0: not yet).
+struct DeviceFacts {
+  std::atomic<int> sms{0}, capability{0};
+};
+DeviceFacts g_facts[64];
+
+int attribute(std::atomic<int>* cached, int dev, cudaDeviceAttr a) {
+  int v = cached ? cached->load(std::memory_order_relaxed) : 0;
+  if (v > 0) return v;
+  if (cudaDeviceGetAttribute(&v, a, dev) != cudaSuccess || v < 0) return 0;
+  if (cached) cached->store(v, std::memory_order_relaxed);
+  return v;
+}
+}  // namespace
+
 int num_sms() {
-  int dev = 0, n = 0;
+  int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+  const int n = attribute(dev < 64 ? &g_facts[dev].sms : nullptr, dev,
+                          cudaDevAttrMultiProcessorCount);
   return n > 0 ? n : 1;
 }
 
 bool device_ok() {
-  int dev = 0, major = 0, minor = 0;
+  int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-    return false;
-  if (cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-    return false;
-  return major == 10 && minor == 3;  // the library is built for sm_103a only
+  std::atomic<int>* cached = dev < 64 ? &g_facts[dev].capability : nullptr;
+  int cc = cached ? cached->load(std::memory_order_relaxed) : 0;
+  if (cc == 0) {
+    cc = attribute(nullptr, dev, cudaDevAttrComputeCapabilityMajor) * 10 +
+         attribute(nullptr, dev, cudaDevAttrComputeCapabilityMinor);
+    if (cached && cc > 0) cached->store(cc, std::memory_order_relaxed);
+  }
+  return cc == 103;  // the library is built for sm_103a only
 }
 
 int64_t chunk_rows(int32_t V) {

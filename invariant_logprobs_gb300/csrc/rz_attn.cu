@@ -1089,8 +1089,8 @@ struct AttnMaps {
 
 template <class E>
 cudaError_t launch(const AttnArgs& a, const AttnMaps& m, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(attn_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kAttnSmem));
+  static SmemOnce once;
+  cudaError_t e = once.set(attn_kernel<E>, static_cast<int>(kAttnSmem));
   if (e != cudaSuccess) return e;
   plan_kernel<<<1, kPlanThreads, 0, st>>>(a);
   e = cudaGetLastError();

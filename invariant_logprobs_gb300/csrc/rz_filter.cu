@@ -1061,9 +1061,8 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
 
 template <class E, bool kResident>
 cudaError_t launch_as(const FilterArgs& a, int64_t T, int parts, size_t smem, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(filter_sample_kernel<E, kResident>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kSmemLimit));
+  static SmemOnce once;
+  const cudaError_t e = once.set(filter_sample_kernel<E, kResident>, static_cast<int>(kSmemLimit));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(T * parts));

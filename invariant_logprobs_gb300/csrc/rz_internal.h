@@ -2,6 +2,7 @@
 // translation units (not part of the public ABI).
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -82,6 +83,26 @@ bool device_ok();  // current device is sm_103 (or newer family member we compil
 
 bool make_tmap_bf16(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer,
                     uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
+
+// Shared memory beyond 48 KB, asked for once per kernel and device: the call
+// takes a microsecond, a tenth of what a small launch costs the host.
+class SmemOnce {
+ public:
+  template <class K>
+  cudaError_t set(K kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done_.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<uint64_t> done_{0};
+};
 
 // A map of 16-bit elements with `rank` <= 5 dimensions (innermost first; strides
 // in bytes of all but the innermost), 128-byte swizzle, zeros outside.

@@ -181,8 +181,7 @@ __device__ __forceinline__ void store8(E* row, bool vec, int V, int col, const f
 
 template <class E>
 __global__ void __launch_bounds__(kKeepThreads) keep_logprob_bwd_kernel(const KeepArgs a) {
-  // last row first: the forward pass before has left the last rows in the L2
-  const long long row = a.T - 1 - blockIdx.x;
+  const long long row = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // not restrict: dlogits may be the logits; every lane loads its columns
   // before it stores them, and no other lane reads them
@@ -238,8 +237,8 @@ cudaError_t launch_fwd(const KeepArgs& a, cudaStream_t st) {
          parts * kKeepWarps < a.chunks)
     parts *= 2;
   const size_t smem = static_cast<size_t>(a.chunks) * (sizeof(float2) + sizeof(uint16_t));
-  cudaError_t e = cudaFuncSetAttribute(keep_logprob_kernel<E>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 196608);
+  static SmemOnce once;
+  const cudaError_t e = once.set(keep_logprob_kernel<E>, 196608);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(a.T * parts));

@@ -415,8 +415,7 @@ RZ_API int rz_logits_loss_fwd_bwd(rz_bf16* logits_inout, const int32_t* tokens,
  * past the free list, a negative page id in a row and a token past n_slots
  * get slot (and table entry) -1 or are dropped, and set RZ_DEVERR_PAGES.
  * B, n_free, n_slots >= 0; page_size, width >= 1; B * width < 2^31.
- * One launch while one block can do it all (B <= 1024 and n_slots <= 16384),
- * else two.  No workspace.  slots_out may be null if n_slots = 0.
+ * One launch, no workspace.  slots_out may be null if n_slots = 0.
  */
 RZ_API int rz_page_tables(const int32_t* lens, const int32_t* new_lens, int32_t B,
                           const int32_t* free_pages, int64_t n_free, int32_t page_size,
@@ -449,9 +448,8 @@ RZ_API int rz_page_tables(const int32_t* lens, const int32_t* new_lens, int32_t 
  * rounded to the inputs' type as the second product's operand.
  * Requires: Hq % Hkv == 0, Hq / Hkv <= 128, D % 8 == 0, 8 <= D <= 128, and
  * 16-byte alignment of q, k_cache, v_cache, out and all strides
- * (RZ_ERR_UNSUPPORTED otherwise), q's strides positive; B, P >= 0.  Page
- * sizes 8, 16, 32, 64 and multiples of 128 are read page by page through
- * tensor maps, all others row by row.
+ * (RZ_ERR_UNSUPPORTED otherwise), q's strides positive; B, P >= 0.  Pages
+ * of a multiple of 8 tokens are read through tensor maps, all others row by row.
  * Lengths past a row's width or negative are cut, page ids outside
  * [0, n_pages) are skipped, a cu_group that is not 0 <= cu[0] <= ... <= B is
  * cut to it: RZ_DEVERR_PAGES / RZ_DEVERR_CU_SEQLENS, no access leaves the

@@ -28,8 +28,8 @@
 //              when a row's maximum has grown by more than 8 (a factor 2^8,
 //              far inside fp32's and fp16's range), so O is rarely rescaled.
 //              Warps without rows only keep step.
-//   warp 8     TMA: query rows, and K and V page by page (page sizes 8, 16, 32,
-//              64 and multiples of 128), one lane a page.
+//   warp 8     TMA: query rows, and K and V in boxes that lie in one page each
+//              (page sizes that are multiples of 8), one lane a box.
 //   warps 9-12 16-byte asynchronous copies for other page sizes, and zeros in
 //              V past a partly filled tile's last token: 0 times a stray NaN
 //              would be NaN.
@@ -83,7 +83,8 @@ struct AttnArgs {
   float scale;  // times log2 e
   int n_pages, page, prefix_width, P, width, B, Hq, Hkv, D, rep, ctas;
   int row_tile;       // query rows per prompt item: whole requests, at most 128
-  int paged_tma;      // pages and tiles fit each other: tiles come by TMA
+  int paged_tma;      // pages are made of whole groups of 8 rows: tiles come by TMA,
+  int unit;           // in boxes of this many rows
   // A K or V tile in its slot: 16 groups of 8 rows x 128 bytes (64 columns),
   // group_bytes apart, the second 64 columns half_bytes behind the first.
   // `fold` says how a page's box is addressed (kFold*).
@@ -376,43 +377,44 @@ __device__ __forceinline__ void load_rows_n(const AttnArgs& a, uint32_t dst, con
   }
 }
 
-// Page ids of the tiles of a part, 32 pages (or, with pages of 128 and more,
-// 32 tiles) to a load, the next load under way while these are used: a load
-// for each tile would put its latency into every tile.
+// Where the tiles of a part lie, in units: runs of tokens that never cross a
+// page (128 at most, the largest power of two that divides the page size).  A
+// load takes the pages of 32 units, the next one under way while these are
+// used: a load for each tile would put its latency into every tile.
 struct PageIds {
   const int32_t* tab;
-  int per_tile;     // pages of a tile; 1 where a page holds whole tiles
   int per_load;     // tiles of a load
-  int t_at, limit;  // tiles of `now` begin here; pages that hold tokens
+  int t_at, limit;  // tiles of `now` begin here; units that hold tokens
   int now, next;
 
   __device__ __forceinline__ int fetch(const AttnArgs& a, int t) const {
-    const int lane = threadIdx.x & 31;
-    const uint32_t j = a.page < kTile
-                           ? static_cast<uint32_t>(t) * per_tile + lane
-                           : static_cast<uint32_t>(t + lane) * kTile / static_cast<uint32_t>(a.page);
-    return j < static_cast<uint32_t>(limit) ? tab[j] : -1;
+    const uint32_t u = static_cast<uint32_t>(t) * (kTile / a.unit) + (threadIdx.x & 31);
+    if (u >= static_cast<uint32_t>(limit)) return -1;
+    return tab[u * static_cast<uint32_t>(a.unit) / static_cast<uint32_t>(a.page)];
   }
   __device__ __forceinline__ void init(const AttnArgs& a, const int32_t* row, int t0, int len) {
     tab = row;
-    per_tile = a.page < kTile ? kTile / a.page : 1;
-    per_load = 32 / per_tile;
+    per_load = a.unit / 4;
     t_at = t0;
-    limit = static_cast<int>((static_cast<uint32_t>(len) + a.page - 1) / a.page);
+    limit = static_cast<int>((static_cast<uint32_t>(len) + a.unit - 1) / a.unit);
     now = fetch(a, t0);
     next = fetch(a, t0 + per_load);
   }
-  // This lane's page of tile t (lanes below n, its pages with tokens); t moves
-  // up by one.  false: a page is not in the pool.
-  __device__ __forceinline__ bool get(const AttnArgs& a, int t, int here, int& pg, int& n) {
+  // This lane's unit of tile t (lanes below n, its units with tokens): its page
+  // and its first row there, in groups of 8; t moves up by one.  false: a page
+  // is not in the pool.
+  __device__ __forceinline__ bool get(const AttnArgs& a, int t, int here, int& pg, int& row8,
+                                      int& n) {
     if (t - t_at >= per_load) {
       t_at += per_load;
       now = next;
       next = fetch(a, t_at + per_load);
     }
-    const int lane = threadIdx.x & 31;
-    n = per_tile == 1 ? 1 : (here + a.page - 1) / a.page;
-    pg = __shfl_sync(0xffffffffu, now, ((t - t_at) * per_tile + lane) & 31);
+    const int lane = threadIdx.x & 31, units = kTile / a.unit;
+    n = (here + a.unit - 1) / a.unit;
+    pg = __shfl_sync(0xffffffffu, now, ((t - t_at) * units + lane) & 31);
+    const uint32_t tok = (static_cast<uint32_t>(t) * units + lane) * a.unit;
+    row8 = static_cast<int>(tok % static_cast<uint32_t>(a.page)) / 8;
     return __all_sync(0xffffffffu, lane >= n || (pg >= 0 && pg < a.n_pages));
   }
 };
@@ -618,14 +620,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       ++item;
       for (int t = w.t0; ok && t < w.t1; ++t, ++tile) {
         const int here = min(w.len - t * kTile, kTile);
-        int pg = 0, n = 0;
-        const bool mine = a.paged_tma && ids.get(a, t, here, pg, n);
-        // in groups of 8 rows: where the tile begins in its page, a box
-        const int row8 = a.page < kTile
-                             ? 0
-                             : static_cast<int>(static_cast<uint32_t>(t) * kTile %
-                                                static_cast<uint32_t>(a.page)) / 8;
-        const uint32_t box8 = (a.page < kTile ? a.page : kTile) / 8;
+        int pg = 0, row8 = 0, n = 0;
+        const bool mine = a.paged_tma && ids.get(a, t, here, pg, row8, n);
+        const uint32_t box8 = a.unit / 8;  // a box, in groups of 8 rows
 #pragma unroll 1
         for (uint32_t kv = 0; kv < 2; ++kv) {
           const uint32_t f = 2 * tile + kv, slot = f % kSlots;
@@ -1191,10 +1188,11 @@ extern "C" int rz_group_decode_attn(const void* q, const int64_t* q_stride, cons
     if (!make_tmap_16bit(&m.q_own, q, 3, dims, st, box)) return RZ_ERR_UNSUPPORTED;
   }
   m.k = m.v = m.q_own;
-  a.paged_tma = n_pages > 0 && page_size % 8 == 0 &&
-                (page_size % kTile == 0 || kTile % page_size == 0);
+  a.paged_tma = n_pages > 0 && page_size % 8 == 0;
+  a.unit = page_size & -page_size;
+  if (a.unit > kTile) a.unit = kTile;
   a.fold = kFoldNone;
-  if (a.paged_tma && D == kMaxD && page_size <= 16) {
+  if (a.paged_tma && D == kMaxD && a.unit <= 16) {
     // small pages: both 64-column halves in one box, interleaved by groups of
     // 8 rows, as each box takes the TMA unit some 58 clocks.  16 x 8 responses
     // of 1,024 to 8,192 tokens, one box and two: pages of 8 tokens 575 and 822
@@ -1213,7 +1211,7 @@ extern "C" int rz_group_decode_attn(const void* q, const int64_t* q_stride, cons
   a.half_bytes = a.fold == kFoldNone ? kHalf : 1024;
   if (a.paged_tma) {
     const uint64_t groups = static_cast<uint64_t>(page_size) / 8;
-    const uint32_t box_groups = static_cast<uint32_t>(page_size < kTile ? page_size : kTile) / 8;
+    const uint32_t box_groups = static_cast<uint32_t>(a.unit) / 8;
     const uint64_t heads = static_cast<uint64_t>(Hkv), pages = static_cast<uint64_t>(n_pages);
     for (int i = 0; i < 2; ++i) {
       const int64_t* s = kv_stride + 3 * i;  // page, token, head

@@ -5,12 +5,17 @@
 //   need_i = ceil((lens_i + new_i) / p) - ceil(lens_i / p),
 //   o_i    = sum_{j < i} need_j,  cu_i = sum_{j < i} new_j,
 //   table[i, ceil(lens_i / p) + j] = free[o_i + j],
-//   slot(cu_i + t) = table[i, (lens_i + t) / p] p + (lens_i + t) % p.
-// The two sums need every earlier request.  Each block adds up all requests
-// before its own (8 bytes each, from L2) instead of waiting for other blocks,
-// so nothing spins and the blocks are independent.  A step's few slots are
-// then written by the same block; an admission's many by a second kernel over
-// the slots, where each finds its request by bisection of cu.
+//   slot(cu_i + t) = page(i, (lens_i + t) / p) p + (lens_i + t) % p,
+// page(i, j) from the row where the request held it, else free[o_i + j - held].
+//
+// One launch.  Both sums need every earlier request: each block adds up all of
+// them before its own group (8 bytes each, from L2) instead of waiting for
+// another block, so nothing spins; and the slots take their pages from the
+// free list, not from the rows that other blocks are writing.  A group of
+// requests has `slices` blocks, which share its slots evenly, so that one long
+// prompt among short ones occupies no single block for long.  Admitting 3,000
+// prompts of up to 2,048 tokens (3.1M slots): two kernels, the second bisecting
+// the sums in global memory for every slot, took 38 us.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -24,9 +29,8 @@ namespace {
 
 constexpr int kPageThreads = 256;
 constexpr int kPageWarps = kPageThreads / 32;
-constexpr int kMaxPer = 1024;           // requests of one block at most
-constexpr int64_t kFusedSlots = 16384;  // slots one block writes itself
-constexpr int kSlotsPerBlock = 2048;
+constexpr int kMaxPer = 1024;          // requests of a group at most
+constexpr int kSlotsPerBlock = 4096;   // wanted
 
 struct PageArgs {
   const int32_t *lens, *news, *free_pages;
@@ -35,11 +39,11 @@ struct PageArgs {
   int32_t* used;
   int* err;
   int64_t n_free, n_slots;
-  int B, page, width, per;
+  int B, page, width, per, slices;
 };
 
 struct Need {
-  int len, add, old_pages, need;  // clamped length, tokens, pages held, pages to take
+  int len, add, held, need;  // clamped length, tokens, pages held, pages to take
 };
 
 __device__ __forceinline__ Need need_of(const PageArgs& a, int i, bool& bad) {
@@ -51,27 +55,15 @@ __device__ __forceinline__ Need need_of(const PageArgs& a, int i, bool& bad) {
     n.len = max(n.len, 0);
     n.add = max(n.add, 0);
   }
-  const long long full = (static_cast<long long>(n.len) + n.add + a.page - 1) / a.page;
-  const long long old = (static_cast<long long>(n.len) + a.page - 1) / a.page;
-  if (full > a.width) bad = true;
-  n.old_pages = static_cast<int>(old < a.width ? old : a.width);
-  n.need = static_cast<int>(full < a.width ? full : a.width) - n.old_pages;
+  // (two lengths below 2^31 add up below 2^32)
+  const uint32_t page = static_cast<uint32_t>(a.page), w = static_cast<uint32_t>(a.width);
+  const uint32_t total = static_cast<uint32_t>(n.len) + static_cast<uint32_t>(n.add);
+  const uint32_t full = total / page + (total % page != 0);
+  const uint32_t held = static_cast<uint32_t>(n.len) / page + (n.len % a.page != 0);
+  if (full > w) bad = true;
+  n.held = static_cast<int>(min(held, w));
+  n.need = static_cast<int>(min(full, w)) - n.held;
   return n;
-}
-
-// The slot of new token t of a request with `len` cached tokens; -1 where the
-// row has no page for it.
-__device__ __forceinline__ long long slot_of(const PageArgs& a, int i, int len, long long t,
-                                             bool& bad) {
-  const long long pos = len + t;
-  const long long j = pos / a.page;
-  if (j >= a.width) return -1;  // flagged with the row's pages
-  const int page = a.table[static_cast<long long>(i) * a.width + j];
-  if (page < 0) {
-    bad = true;
-    return -1;
-  }
-  return static_cast<long long>(page) * a.page + (pos - j * a.page);
 }
 
 __device__ __forceinline__ longlong2 block_sum2(longlong2 v, longlong2* scratch) {
@@ -92,16 +84,19 @@ __device__ __forceinline__ longlong2 block_sum2(longlong2 v, longlong2* scratch)
   return s;
 }
 
-__global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs a, bool fused) {
+__global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs a) {
   __shared__ longlong2 scratch[kPageWarps];
   __shared__ long long s_first[kMaxPer], s_cu[kMaxPer + 1];
-  const int begin = blockIdx.x * a.per;
+  __shared__ int2 s_len[kMaxPer];  // length, pages held
+  const int group = blockIdx.x / a.slices, slice = blockIdx.x % a.slices;
+  const int begin = group * a.per;
   const int count = min(a.per, a.B - begin);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   bool bad = false;
 
   longlong2 before = make_longlong2(0, 0);
   if (begin > 0) {
+#pragma unroll 4
     for (int i = threadIdx.x; i < begin; i += kPageThreads) {
       const Need n = need_of(a, i, bad);
       before.x += n.need;
@@ -109,13 +104,14 @@ __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs
     }
     before = block_sum2(before, scratch);
   }
-  // exclusive sums of the block's own requests, a round of threads at a time
+  // exclusive sums of the group's own requests, a round of threads at a time
   for (int r = 0; r < count; r += kPageThreads) {
     const int i = r + threadIdx.x;
     longlong2 v = make_longlong2(0, 0);
     if (i < count) {
       const Need n = need_of(a, begin + i, bad);
       v = make_longlong2(n.need, n.add);
+      s_len[i] = make_int2(n.len, n.held);
     }
     longlong2 inc = v;
 #pragma unroll
@@ -141,13 +137,14 @@ __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs
     if (i < count) {
       s_first[i] = base.x + inc.x - v.x;
       s_cu[i] = base.y + inc.y - v.y;
-      a.cu[begin + i] = s_cu[i];
+      if (slice == 0) a.cu[begin + i] = s_cu[i];
     }
     __syncthreads();
   }
+  const bool last = begin + count == a.B;
   if (threadIdx.x == 0) {
     s_cu[count] = before.y;
-    if (begin + count == a.B) {
+    if (last && slice == 0) {
       a.cu[a.B] = before.y;
       *a.used = static_cast<int32_t>(before.x < 0x7fffffffLL ? before.x : 0x7fffffffLL);
       if (before.y > a.n_slots) bad = true;
@@ -155,64 +152,52 @@ __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs
   }
   __syncthreads();
 
-  // new table entries, a warp per request
-  for (int i = warp; i < count; i += kPageWarps) {
+  // the rows' new entries, a warp a request
+  for (int i = slice * kPageWarps + warp; i < count; i += a.slices * kPageWarps) {
     const Need n = need_of(a, begin + i, bad);
-    int32_t* row = a.table + static_cast<long long>(begin + i) * a.width + n.old_pages;
+    int32_t* row = a.table + static_cast<long long>(begin + i) * a.width + n.held;
     for (int j = lane; j < n.need; j += 32) {
       const long long f = s_first[i] + j;
       if (f >= a.n_free) bad = true;
       row[j] = f < a.n_free ? a.free_pages[f] : -1;
     }
   }
-  if (fused) {
-    __syncthreads();  // the block wrote every entry that its slots read
-    const long long total = s_cu[count];
-    for (long long t = threadIdx.x; t < a.n_slots; t += kPageThreads) {
-      long long slot = -1;
-      if (t < total) {
-        int lo = 0, hi = count;  // the last i with cu_i <= t: cu[lo] <= t < cu[hi]
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (s_cu[mid] <= t) lo = mid;
-          else hi = mid;
-        }
-        slot = slot_of(a, begin + lo, max(a.lens[begin + lo], 0), t - s_cu[lo], bad);
-      }
-      a.slots[t] = slot;
-    }
-  }
-  if (bad && a.err) atomicOr(a.err, RZ_DEVERR_PAGES);
-}
 
-__global__ void __launch_bounds__(kPageThreads) page_slot_kernel(const PageArgs a) {
-  __shared__ int s_range[2];
-  const long long t0 = static_cast<long long>(blockIdx.x) * kSlotsPerBlock;
-  const long long t1 = min(t0 + kSlotsPerBlock, static_cast<long long>(a.n_slots));
-  bool bad = false;
-  // the requests of the block's first and last slot bound every bisection
-  if (threadIdx.x < 2) {
-    const long long t = threadIdx.x == 0 ? t0 : t1 - 1;
-    int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.cu[mid] <= t) lo = mid;
-      else hi = mid;
-    }
-    s_range[threadIdx.x] = lo;
+  // the group's slots (the last group: and what is past all tokens), a slice of
+  // them in a run
+  const long long t_begin = count > 0 ? s_cu[0] : 0, total = s_cu[count];
+  const long long t_end = min(last ? static_cast<long long>(a.n_slots) : total,
+                              static_cast<long long>(a.n_slots));
+  if (t_begin >= t_end) {
+    if (bad && a.err) atomicOr(a.err, RZ_DEVERR_PAGES);
+    return;
   }
-  __syncthreads();
-  const long long total = a.cu[a.B];
+  const long long run = (t_end - t_begin + a.slices - 1) / a.slices;
+  const long long t0 = t_begin + slice * run, t1 = min(t0 + run, t_end);
+  const uint32_t page = static_cast<uint32_t>(a.page);
   for (long long t = t0 + threadIdx.x; t < t1; t += kPageThreads) {
     long long slot = -1;
     if (t < total) {
-      int lo = s_range[0], hi = s_range[1] + 1;
+      int lo = 0, hi = count;  // the last i with cu_i <= t: cu[lo] <= t < cu[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.cu[mid] <= t) lo = mid;
+        if (s_cu[mid] <= t) lo = mid;
         else hi = mid;
       }
-      slot = slot_of(a, lo, max(a.lens[lo], 0), t - a.cu[lo], bad);
+      const int2 held = s_len[lo];
+      const uint32_t pos = static_cast<uint32_t>(held.x) + static_cast<uint32_t>(t - s_cu[lo]);
+      const uint32_t j = pos / page;
+      if (j < static_cast<uint32_t>(a.width)) {  // (else flagged with the row's pages)
+        int pg;
+        if (j < static_cast<uint32_t>(held.y)) {
+          pg = a.table[static_cast<long long>(begin + lo) * a.width + j];
+        } else {
+          const long long f = s_first[lo] + (j - held.y);
+          pg = f < a.n_free ? a.free_pages[f] : -1;
+        }
+        if (pg < 0) bad = true;
+        else slot = static_cast<long long>(pg) * a.page + (pos - j * page);
+      }
     }
     a.slots[t] = slot;
   }
@@ -238,20 +223,15 @@ extern "C" int rz_page_tables(const int32_t* lens, const int32_t* new_lens, int3
   if (!device_ok()) return RZ_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   PageArgs a{lens, new_lens, free_pages, table, slots_out, cu_out, used_out, err_flag,
-             n_free, n_slots, B, page_size, width, kMaxPer};
-  const bool fused = B <= kMaxPer && n_slots <= kFusedSlots;
-  if (!fused) {
-    // about one block an SM; a block adds up what comes before it, so small
-    // batches take few requests a block and large ones few blocks
-    a.per = 64;
-    while (a.per < kMaxPer && static_cast<int64_t>(a.per) * num_sms() < B) a.per *= 2;
-  }
-  const int blocks = B > 0 ? (B + a.per - 1) / a.per : 1;
-  ProfScope ps(RZ_PROF_SMALL, fused ? 1 : 2, st);
-  page_table_kernel<<<blocks, kPageThreads, 0, st>>>(a, fused);
-  if (!fused && n_slots > 0) {
-    const int64_t nb = (n_slots + kSlotsPerBlock - 1) / kSlotsPerBlock;
-    page_slot_kernel<<<static_cast<unsigned>(nb), kPageThreads, 0, st>>>(a);
-  }
+             n_free, n_slots, B, page_size, width, 64, 1};
+  // about one group an SM at most: a block adds up what comes before its group,
+  // so a small batch takes small groups and a large one few
+  while (a.per < kMaxPer && static_cast<int64_t>(a.per) * num_sms() < B) a.per *= 2;
+  const int64_t groups = B > 0 ? (B + a.per - 1) / a.per : 1;
+  const int64_t slices = (n_slots + groups * kSlotsPerBlock - 1) / (groups * kSlotsPerBlock);
+  const int64_t most = (int64_t(1) << 30) / groups;
+  a.slices = static_cast<int>(slices < 1 ? 1 : (slices < most ? slices : most));
+  ProfScope ps(RZ_PROF_SMALL, 1, st);
+  page_table_kernel<<<static_cast<unsigned>(groups * a.slices), kPageThreads, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? RZ_OK : RZ_ERR_CUDA;
 }

@@ -129,7 +129,8 @@ def test_matches_the_formula(rz, case):
 
 @pytest.mark.parametrize("layout", ["plain", "heads_first", "side_by_side"])
 @pytest.mark.parametrize("fill", [float("nan"), float("inf")])
-@pytest.mark.parametrize("D,page", [(64, 16), (128, 16), (128, 256), (96, 32), (128, 40)])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 16), (128, 256), (96, 32), (128, 40),
+                                    (128, 20), (64, 48)])
 def test_strides_and_what_lies_past_the_lengths(rz, layout, fill, D, page):
     """Other cache layouts; NaN or inf in every place that holds no token."""
     a = _build(BF, 8, 2, D, page, [2, 3], [77, 300], [1, 40, 0, 129, 16], seed=5, layout=layout,

@@ -175,31 +175,59 @@ __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs
   const long long run = (t_end - t_begin + a.slices - 1) / a.slices;
   const long long t0 = t_begin + slice * run, t1 = min(t0 + run, t_end);
   const uint32_t page = static_cast<uint32_t>(a.page);
-  for (long long t = t0 + threadIdx.x; t < t1; t += kPageThreads) {
-    long long slot = -1;
-    if (t < total) {
-      int lo = 0, hi = count;  // the last i with cu_i <= t: cu[lo] <= t < cu[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_cu[mid] <= t) lo = mid;
-        else hi = mid;
-      }
-      const int2 held = s_len[lo];
-      const uint32_t pos = static_cast<uint32_t>(held.x) + static_cast<uint32_t>(t - s_cu[lo]);
-      const uint32_t j = pos / page;
-      if (j < static_cast<uint32_t>(a.width)) {  // (else flagged with the row's pages)
-        int pg;
-        if (j < static_cast<uint32_t>(held.y)) {
-          pg = a.table[static_cast<long long>(begin + lo) * a.width + j];
-        } else {
-          const long long f = s_first[lo] + (j - held.y);
-          pg = f < a.n_free ? a.free_pages[f] : -1;
-        }
-        if (pg < 0) bad = true;
-        else slot = static_cast<long long>(pg) * a.page + (pos - j * page);
-      }
+  // (a page past the row's width is flagged with the row's entries)
+  const auto page_of = [&](int i, uint32_t j) {
+    if (j >= static_cast<uint32_t>(a.width)) return -1;
+    const int held = s_len[i].y;
+    int pg;
+    if (j < static_cast<uint32_t>(held)) {
+      pg = a.table[static_cast<long long>(begin + i) * a.width + j];
+    } else {
+      const long long f = s_first[i] + (j - held);
+      pg = f < a.n_free ? a.free_pages[f] : -1;
     }
-    a.slots[t] = slot;
+    if (pg < 0) bad = true;
+    return pg;
+  };
+  int top = 1;
+  while (top < count) top *= 2;
+  const bool wide = (reinterpret_cast<uintptr_t>(a.slots) & 15u) == 0;
+  // four slots a thread: one search and one division for them, unless a
+  // request ends among them
+  for (long long t4 = (t0 & ~3ll) + 4 * threadIdx.x; t4 < t1; t4 += 4 * kPageThreads) {
+    long long out[4], next = -1;
+    int i = 0, pg = -1;
+    uint32_t j = 0, off = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const long long t = t4 + q;
+      out[q] = -1;
+      if (t < t0 || t >= t1 || t >= total) continue;
+      if (t >= next) {
+        i = 0;  // the last with cu_i <= t
+        for (int s = top >> 1; s > 0; s >>= 1)
+          if (i + s < count && s_cu[i + s] <= t) i += s;
+        next = s_cu[i + 1];
+        const uint32_t pos =
+            static_cast<uint32_t>(s_len[i].x) + static_cast<uint32_t>(t - s_cu[i]);
+        j = pos / page;
+        off = pos - j * page;
+        pg = page_of(i, j);
+      } else if (++off == page) {
+        off = 0;
+        pg = page_of(i, ++j);
+      }
+      if (pg >= 0) out[q] = static_cast<long long>(pg) * a.page + off;
+    }
+    if (wide && t4 >= t0 && t4 + 4 <= t1) {
+      longlong2* dst = reinterpret_cast<longlong2*>(a.slots + t4);
+      dst[0] = make_longlong2(out[0], out[1]);
+      dst[1] = make_longlong2(out[2], out[3]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (t4 + q >= t0 && t4 + q < t1) a.slots[t4 + q] = out[q];
+    }
   }
   if (bad && a.err) atomicOr(a.err, RZ_DEVERR_PAGES);
 }

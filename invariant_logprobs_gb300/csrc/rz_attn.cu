@@ -1124,8 +1124,9 @@ extern "C" int rz_group_decode_attn(const void* q, const int64_t* q_stride, cons
     return RZ_ERR_INVALID_ARG;
   if (width < 0 || prefix_width < 0 || !(scale == scale)) return RZ_ERR_INVALID_ARG;
   if (dtype != RZ_DTYPE_BF16 && dtype != RZ_DTYPE_F16) return RZ_ERR_INVALID_ARG;
-  if (P > 0 && (!prefix_table || !prefix_lens || !cu_group)) return RZ_ERR_INVALID_ARG;
-  if (B > 0 && (!q || !q_stride || !kv_stride || !table || !lens || !out))
+  if (P > 0 && ((prefix_width > 0 && !prefix_table) || !prefix_lens || !cu_group))
+    return RZ_ERR_INVALID_ARG;
+  if (B > 0 && (!q || !q_stride || !kv_stride || (width > 0 && !table) || !lens || !out))
     return RZ_ERR_INVALID_ARG;
   if (B > 0 && n_pages > 0 && (!k_cache || !v_cache)) return RZ_ERR_INVALID_ARG;
   if (static_cast<int64_t>(B) + P >= (1 << 30) || static_cast<int64_t>(B) * Hq >= (1 << 30))

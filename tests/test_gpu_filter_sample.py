@@ -121,12 +121,12 @@ def test_full_vocabulary(rz, dtype):
         assert torch.equal(x.repeat(40, *[1] * (x.dim() - 1)), b)
 
 
-def test_wide_vocabulary(rz):
-    """A row past what the SMs' shared memory holds together."""
-    V = 3_000_001
+@pytest.mark.parametrize("V,dtype", [(3_000_001, "f32"), (1_000_000, "bf16"), (1 << 24, "f16")])
+def test_wide_vocabulary(rz, V, dtype):
+    """Rows past what a cluster's shared memory holds, up to the largest."""
     g = torch.Generator(device=DEV)
     g.manual_seed(4)
-    z = torch.randn(2, V, generator=g, device=DEV)
+    z = torch.randn(2, V, generator=g, device=DEV).to(DT[dtype])
     u = torch.rand(2, generator=g, device=DEV)
     p = _t([0.7, 1.0])
     tok, lp, n, keep = rz.rz_filter_sample(z, u, top_p=p, want_keep=True)
@@ -135,7 +135,13 @@ def test_wide_vocabulary(rz):
                                    float(u[r]))
         assert (int(tok[r]), int(n[r])) == (a, len(kept))
         assert abs(float(lp[r]) - want) <= 1e-5 * (1 + abs(want))
-    assert torch.equal(rz.rz_keep_logprob(z, tok, keep=keep)[0], lp)
+    lp2, lse = rz.rz_keep_logprob(z, tok, keep=keep)
+    assert torch.equal(lp2, lp)
+    d = rz.rz_keep_logprob_bwd(z, tok, lse, torch.ones(2, device=DEV), keep=keep)
+    p_tok = torch.exp(lp.double())
+    got = d.double().gather(1, tok.long()[:, None])[:, 0]
+    eps = torch.finfo(d.dtype).eps
+    assert ((got - (1 - p_tok)).abs() <= eps).all()
 
 
 def test_no_filters_at_all_and_row_strides(rz):

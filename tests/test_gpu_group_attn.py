@@ -173,6 +173,19 @@ def test_requests_outside_every_group(rz):
     _check(b, out, lse)
 
 
+def test_no_pages_at_all(rz):
+    """Tables without a column and a pool without a page."""
+    a = _build(HF, 4, 2, 64, 16, [2], [50], [0, 0], seed=12)
+    own = {**a, "table": a["table"][:, :0].contiguous()}
+    _check(own, *rz.rz_group_decode_attn(**own))
+    none = {**own, "prefix_table": a["prefix_table"][:, :0].contiguous(),
+            "prefix_lens": torch.zeros_like(a["prefix_lens"]), "k_cache": a["k_cache"][:0],
+            "v_cache": a["v_cache"][:0]}
+    err = rz.new_err_flag(DEV)
+    out, lse = rz.rz_group_decode_attn(**none, err_flag=err)
+    assert not out.any() and (lse == -math.inf).all() and err.item() == 0
+
+
 def test_bad_tables_are_flagged_and_skipped(rz):
     a = _build(BF, 4, 2, 64, 16, [2, 1], [40, 33], [20, 21, 22], seed=9)
     want, _ = rz.rz_group_decode_attn(**a)

@@ -1,0 +1,172 @@
+"""A group rollout over a paged cache, and the learner that scores it.
+
+P prompts with G responses each run through a one-layer attention model with
+random weights (there is no checkpoint here): every step
+
+* rz_page_tables gives the new token of each response a page and a slot,
+* torch writes its key and value there,
+* rz_group_decode_attn attends over the prompt's pages, read once for the
+  group, and the response's own,
+* rz_lmhead_logits and rz_filter_sample draw the next token under each
+  response's filters and record log mu under what they kept.
+
+The learner then scores the recorded tokens under the recorded kept sets
+(rz_keep_logprob), takes the importance-sampled loss (rz_is_loss) and the
+gradient of the logits (rz_keep_logprob_bwd).  With the rollout's own weights
+every log pi equals its log mu bit for bit, so w = 1 and D3 = 0.
+
+    python examples/group_rollout.py [--prompts 4] [--group 8] [--steps 32]
+"""
+
+import argparse
+import os
+import sys
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+import invariant_logprobs_gb300 as rz  # noqa: E402
+
+HEADS, KV_HEADS, HEAD, PAGE = 8, 2, 64, 16
+WIDTH = HEADS * HEAD
+
+
+class Model:
+    """Embedding, one attention layer with a residual, LM head."""
+
+    def __init__(self, V, g):
+        def weight(*shape, std):
+            return (torch.randn(*shape, generator=g, device="cuda") * std).to(torch.bfloat16)
+
+        self.embed = weight(V, WIDTH, std=1.0)
+        self.q = weight(WIDTH, WIDTH, std=WIDTH ** -0.5)
+        self.kv = weight(WIDTH, 2 * KV_HEADS * HEAD, std=WIDTH ** -0.5)
+        self.o = weight(WIDTH, WIDTH, std=WIDTH ** -0.5)
+        self.head = weight(V, WIDTH, std=0.1)
+
+    def qkv(self, tokens):
+        x = self.embed[tokens.long()]
+        kv = (x @ self.kv).view(-1, 2, KV_HEADS, HEAD)
+        return x, (x @ self.q).view(-1, HEADS, HEAD), kv[:, 0], kv[:, 1]
+
+    def hidden(self, x, attention):
+        return x + attention.reshape(-1, WIDTH) @ self.o
+
+
+class Cache:
+    """A pool of pages; the tables hand out `free` in order."""
+
+    def __init__(self, n_pages):
+        shape = (n_pages, PAGE, KV_HEADS, HEAD)
+        self.k = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+        self.v = torch.empty_like(self.k)
+        self.free = torch.randperm(n_pages, device="cuda").to(torch.int32)
+
+    def extend(self, table, lens, new, n_new, err):
+        """Pages and slots for the new tokens; lens moves on by them."""
+        slots, _, used = rz.rz_page_tables(lens, new, self.free, PAGE, table, n_new, err_flag=err)
+        self.free = self.free[int(used):].contiguous()
+        lens += new
+        return slots
+
+    def write(self, slots, k, v):
+        self.k.view(-1, KV_HEADS, HEAD)[slots] = k
+        self.v.view(-1, KV_HEADS, HEAD)[slots] = v
+
+
+def rollout(model, prompts, group, steps, filters, uniforms, err):
+    """prompts: list of token tensors.  Returns what the learner needs, a step
+    per entry: hidden states, tokens, log mu, kept sets."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    P, B = len(prompts), len(prompts) * group
+    # the prompt's last token is each response's first own one
+    lengths = [len(p) - 1 for p in prompts]
+    own_pages = -(-steps // PAGE)
+    cache = Cache(sum(-(-n // PAGE) for n in lengths) + B * own_pages)
+    prefix_table = torch.full((P, -(-max(lengths) // PAGE)), -1, **i32)
+    prefix_lens = torch.zeros(P, **i32)
+    slots = cache.extend(prefix_table, prefix_lens, torch.tensor(lengths, **i32), sum(lengths), err)
+    _, _, k, v = model.qkv(torch.cat([p[:-1] for p in prompts]))
+    cache.write(slots, k, v)
+
+    cu_group = torch.arange(P + 1, **i32) * group
+    table, lens = torch.full((B, own_pages), -1, **i32), torch.zeros(B, **i32)
+    one = torch.ones(B, **i32)
+    tokens = torch.stack([p[-1] for p in prompts]).repeat_interleave(group).to(torch.int32)
+    record = []
+    for step in range(steps):
+        x, q, k, v = model.qkv(tokens)
+        cache.write(cache.extend(table, lens, one, B, err), k, v)
+        attention, _ = rz.rz_group_decode_attn(q, cache.k, cache.v, table, lens,
+                                               prefix_table=prefix_table, prefix_lens=prefix_lens,
+                                               cu_group=cu_group, err_flag=err)
+        hidden = model.hidden(x, attention)
+        logits = rz.rz_lmhead_logits(hidden, model.head, err_flag=err)
+        tokens, logmu, kept, keep = rz.rz_filter_sample(logits, uniforms[step], want_keep=True,
+                                                        err_flag=err, **filters)
+        record.append((hidden, tokens, logmu, keep))
+    return record
+
+
+def learn(model, record, filters, rewards, group, err):
+    """Loss, D3 and the gradients of the LM head and its inputs."""
+    steps, B = len(record), len(record[0][1])
+
+    def by_response(i):  # [steps, B, ...] -> [B * steps, ...]
+        return torch.stack([r[i] for r in record], 1).flatten(0, 1).contiguous()
+
+    hidden, tokens, logmu, keep = (by_response(i) for i in range(4))
+    temperature = filters["temperature"].repeat_interleave(steps)
+    logits = rz.rz_lmhead_logits(hidden, model.head, err_flag=err)
+    logpi, lse = rz.rz_keep_logprob(logits, tokens, keep=keep, temperature=temperature,
+                                    err_flag=err)
+    cu = torch.arange(B + 1, dtype=torch.int64, device="cuda") * steps
+    adv = rz.rz_group_advantage(rewards, group)
+    coef = torch.empty(B * steps, device="cuda")
+    loss, d3, _ = rz.rz_is_loss(logpi, logmu, cu, adv, coef_out=coef, err_flag=err)
+    # coef is minus the loss's derivative; the logits are not needed any more
+    dz = rz.rz_keep_logprob_bwd(logits, tokens, lse, -coef, keep=keep, temperature=temperature,
+                                dlogits_out=logits, err_flag=err)
+    return {"loss": loss, "d3": d3, "logpi": logpi, "logmu": logmu,
+            "dH": dz @ model.head.float(), "dW": dz.T @ hidden.float()}
+
+
+def run(n_prompts=4, group=8, steps=32, V=5003, seed=0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    model = Model(V, g)
+    prompts = [torch.randint(0, V, (40 + 37 * i,), generator=g, device="cuda")
+               for i in range(n_prompts)]
+    B = n_prompts * group
+    row = torch.arange(B, device="cuda")
+    filters = {"temperature": 0.7 + 0.1 * (row % 7).float(),
+               "top_k": torch.where(row % 3 == 0, 50, 0).to(torch.int32),
+               "top_p": torch.where(row % 2 == 0, 0.95, 1.0),
+               "min_p": torch.where(row % 5 == 0, 0.02, 0.0)}
+    uniforms = torch.rand(steps, B, generator=g, device="cuda")
+    err = rz.new_err_flag("cuda")
+    record = rollout(model, prompts, group, steps, filters, uniforms, err)
+    rewards = torch.rand(B, generator=g, device="cuda")
+    out = learn(model, record, filters, rewards, group, err)
+    if int(err):
+        raise RuntimeError("device error flags %d" % int(err))
+    return out
+
+
+def main():
+    p = argparse.ArgumentParser(description=__doc__.split("\n")[0])
+    p.add_argument("--prompts", type=int, default=4)
+    p.add_argument("--group", type=int, default=8)
+    p.add_argument("--steps", type=int, default=32)
+    p.add_argument("--vocab", type=int, default=5003)
+    a = p.parse_args()
+    out = run(a.prompts, a.group, a.steps, a.vocab)
+    same = torch.equal(out["logpi"], out["logmu"])
+    print("tokens %d  loss %.6f  D3 %g  log pi == log mu: %s  |dH| %.4g  |dW| %.4g"
+          % (len(out["logpi"]), float(out["loss"]), float(out["d3"]), same,
+             float(out["dH"].norm()), float(out["dW"].norm())))
+
+
+if __name__ == "__main__":
+    main()

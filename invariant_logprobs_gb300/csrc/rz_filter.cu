@@ -98,16 +98,33 @@ __device__ __forceinline__ uint64_t mass_target(uint64_t x, uint64_t f) {
   return t > 0 ? t : 1;
 }
 
-// A list entry orders as the row does: the key, then the lower index.
-__device__ __forceinline__ uint64_t entry_of(float z, int v) {
-  return static_cast<uint64_t>(order_key(z)) << 32 | static_cast<uint32_t>(~v);
-}
-__device__ __forceinline__ float entry_value(uint64_t e) {
-  return key_value(static_cast<uint32_t>(e >> 32));
-}
-__device__ __forceinline__ int entry_index(uint64_t e) {
-  return static_cast<int>(~static_cast<uint32_t>(e));
-}
+// A list entry orders as the row does: the key, then the lower index, in as few
+// bits as tell them apart (the key's that its type has, the index's that V has),
+// so that a split of the entries' range parts equal logits too.
+template <class E>
+struct KeyDrop;  // low bits that are the same in every key of a sign
+template <>
+struct KeyDrop<float> { static constexpr int value = 0; };
+template <>
+struct KeyDrop<__nv_bfloat16> { static constexpr int value = 16; };
+template <>
+struct KeyDrop<__half> { static constexpr int value = 13; };
+template <class E>
+struct Entries {
+  static constexpr int kDrop = KeyDrop<E>::value;
+  int lg;  // 2^lg >= V
+  __device__ __forceinline__ uint32_t last() const { return (1u << lg) - 1; }
+  __device__ __forceinline__ uint64_t of(float z, int v) const {
+    return static_cast<uint64_t>(order_key(z) >> kDrop) << lg | (last() - v);
+  }
+  __device__ __forceinline__ float value(uint64_t e) const {
+    const uint32_t k = static_cast<uint32_t>(e >> lg) << kDrop;
+    return key_value(k & 0x80000000u ? k : k | ((1u << kDrop) - 1));
+  }
+  __device__ __forceinline__ int index(uint64_t e) const {
+    return static_cast<int>(last() - (static_cast<uint32_t>(e) & last()));
+  }
+};
 
 struct FilterShared {
   uint32_t table[kFixTable];
@@ -118,9 +135,9 @@ struct FilterShared {
   struct {
     uint32_t count[256], lo[256], hi[256];
   } digit;
-  uint64_t few[32], range[2];
+  uint64_t few[32];
   int n_few;
-  uint64_t red[kFilterWarps];
+  uint64_t red[2 * kFilterWarps];
   float redf[2 * kFilterWarps];
   // written by every CTA of the cluster
   float part_max[kMaxParts], part_min[kMaxParts];
@@ -195,6 +212,12 @@ __device__ __forceinline__ Tv warp_sum(Tv x) {
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
+// The same of x < 2^48, as two sums of 24 bits a lane.
+__device__ __forceinline__ uint64_t warp_sum48(uint64_t x) {
+  const uint32_t lo = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(x) & 0xffffffu);
+  const uint32_t hi = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(x >> 24));
+  return (static_cast<uint64_t>(hi) << 24) + lo;
+}
 __device__ __forceinline__ uint64_t block_sum(FilterShared& s, uint64_t x) {
   x = warp_sum(x);
   __syncthreads();
@@ -227,6 +250,42 @@ __device__ __forceinline__ Tv block_scan(Tv* scratch, Tv x, Tv& total) {
     total += v;
   }
   return base + inc - x;
+}
+
+// The same of two sums at once.
+__device__ __forceinline__ void block_scan2(uint64_t* scratch, uint64_t x, uint64_t y,
+                                            uint64_t& x_at, uint64_t& y_at, uint64_t& x_all,
+                                            uint64_t& y_all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint64_t ix = x, iy = y;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t tx = __shfl_up_sync(0xffffffffu, ix, o);
+    const uint64_t ty = __shfl_up_sync(0xffffffffu, iy, o);
+    if (lane >= o) {
+      ix += tx;
+      iy += ty;
+    }
+  }
+  __syncthreads();
+  if (lane == 31) {
+    scratch[2 * warp] = ix;
+    scratch[2 * warp + 1] = iy;
+  }
+  __syncthreads();
+  x_at = ix - x;
+  y_at = iy - y;
+  x_all = y_all = 0;
+#pragma unroll
+  for (int w = 0; w < kFilterWarps; ++w) {
+    const uint64_t a = scratch[2 * w], b = scratch[2 * w + 1];
+    if (w < warp) {
+      x_at += a;
+      y_at += b;
+    }
+    x_all += a;
+    y_all += b;
+  }
 }
 
 // ------------------------------------------------------------------ selection
@@ -282,8 +341,9 @@ __device__ __forceinline__ void digit_find(FilterShared& s, uint64_t target, uin
 // above it amount to less than `target`, and that amount.  Entries are in a
 // total order, so ties need no care.  The entries' range is split 256 ways
 // until a warp can hold what is left.
-__device__ uint64_t select_list(FilterShared& s, const FixScale& scale, bool mass, int n,
-                                uint64_t target) {
+template <class E>
+__device__ uint64_t select_list(FilterShared& s, const FixScale& scale, const Entries<E>& en,
+                                bool mass, int n, uint64_t target) {
   const int lane = threadIdx.x & 31;
   uint64_t lo = ~0ull, hi = 0;
   for (int i = threadIdx.x; i < n; i += kFilterThreads) {
@@ -297,18 +357,18 @@ __device__ uint64_t select_list(FilterShared& s, const FixScale& scale, bool mas
     lo = x < lo ? x : lo;
     hi = y > hi ? y : hi;
   }
-  if (threadIdx.x == 0) {
-    s.range[0] = ~0ull;
-    s.range[1] = 0;
+  __syncthreads();
+  if (lane == 0) {
+    s.red[threadIdx.x >> 5] = lo;
+    s.red[kFilterWarps + (threadIdx.x >> 5)] = hi;
   }
   __syncthreads();
-  if (lane == 0 && lo <= hi) {
-    atomicMin(reinterpret_cast<unsigned long long*>(&s.range[0]), lo);
-    atomicMax(reinterpret_cast<unsigned long long*>(&s.range[1]), hi);
+#pragma unroll
+  for (int w = 0; w < kFilterWarps; ++w) {
+    const uint64_t x = s.red[w], y = s.red[kFilterWarps + w];
+    lo = x < lo ? x : lo;
+    hi = y > hi ? y : hi;
   }
-  __syncthreads();
-  lo = s.range[0];
-  hi = s.range[1];
   uint64_t above = 0;
   while (true) {
     const uint64_t width = hi - lo;
@@ -322,7 +382,7 @@ __device__ uint64_t select_list(FilterShared& s, const FixScale& scale, bool mas
       if (e < lo || e > hi) continue;
       const uint32_t b = static_cast<uint32_t>((e - lo) >> sh);
       digit_add(s, b, 1, false);
-      if (mass) digit_add(s, b, fix_weight(scale, s.table, entry_value(e)), true);
+      if (mass) digit_add(s, b, fix_weight(scale, s.table, en.value(e)), true);
     }
     __syncthreads();
     if (threadIdx.x < 32)
@@ -347,7 +407,7 @@ __device__ uint64_t select_list(FilterShared& s, const FixScale& scale, bool mas
   if (threadIdx.x < 32) {
     const int m = min(s.n_few, 32);
     const uint64_t e = lane < m ? s.few[lane] : 0;
-    const uint64_t w = lane < m ? (mass ? fix_weight(scale, s.table, entry_value(e)) : 1) : 0;
+    const uint64_t w = lane < m ? (mass ? fix_weight(scale, s.table, en.value(e)) : 1) : 0;
     uint64_t up = above;
     for (int i = 0; i < m; ++i) {
       const uint64_t o = __shfl_sync(0xffffffffu, e, i), x = __shfl_sync(0xffffffffu, w, i);
@@ -436,6 +496,12 @@ __device__ void select_row(FilterShared& s, cg::cluster_group& cluster, const Fi
 }
 
 // ------------------------------------------------------------------ bins
+// Steps of y from `lo`, `width` of them (0: none).
+struct Steps {
+  uint32_t lo, width;
+  __device__ __forceinline__ bool has(uint32_t k) const { return k - lo < width; }
+};
+
 // Bins of a row: 2^sh of the weights' steps of 2^-10 in y each, the last one
 // open.  Their order agrees with the logits'.
 struct Binning {
@@ -446,6 +512,12 @@ struct Binning {
   __device__ __forceinline__ int bin(const FixScale& s, float z) const {
     float r;
     return bin(s.big ? fix_steps<true>(s, z, r) : fix_steps<false>(s, z, r));
+  }
+  // The steps of bins b0 .. b1 (none if b1 < b0).
+  __device__ __forceinline__ Steps steps(int b0, int b1) const {
+    const uint32_t lo = static_cast<uint32_t>(b0) << sh;
+    const uint32_t end = b1 == kBins - 1 ? ~0u : static_cast<uint32_t>(b1 + 1) << sh;
+    return Steps{lo, b1 < b0 ? 0u : end - lo};
   }
   // Bounds on the weight of what is in bin b (y within a step of its k).
   __device__ __forceinline__ uint64_t most(const uint32_t* tab, int drop, int b) const {
@@ -475,21 +547,18 @@ __device__ __forceinline__ void count_bins(FilterShared& s, const FixScale& scal
   }
 }
 
-// Pass 3: (kMass) exact masses by blocks of what lies in bins below bin_lo, and
-// of what lies between bin_hi and bin_k; what is in bin_lo .. bin_hi and bin_k
-// is listed.  Returns (lane 0: of its warp's blocks; all lanes: of their columns).
-template <bool kBig, bool kMass, class E>
+// Pass 3: (kMass) exact masses by blocks of what lies above the band, and of all
+// that lies above bin_k; (kCutK) what is in bin_k and (kMass) in the band is
+// listed.  Returns (lane 0: of its warp's blocks; all lanes: of their columns).
+template <bool kBig, bool kMass, bool kCutK, class E>
 __device__ __forceinline__ void sum_masses(FilterShared& s, const FixScale& scale,
-                                           const Binning& bn, const E* z, bool vec, int v0, int n,
-                                           int bin_k, int bin_lo, int bin_hi,
-                                           uint64_t* block_mass, uint64_t& sum_a,
-                                           uint64_t& sum_r) {
+                                           const Entries<E>& en, const E* z, bool vec, int v0,
+                                           int n, Steps of_k, Steps band, uint64_t* block_mass,
+                                           uint64_t& sum_a, uint64_t& sum_all) {
   const int lane = threadIdx.x & 31;
-  const uint32_t band = static_cast<uint32_t>(bin_hi - bin_lo);  // (empty: bin_hi < bin_lo)
-  const bool any_band = bin_hi >= bin_lo;
   for (int blk = threadIdx.x >> 5; blk * kBlock < n; blk += kFilterWarps) {
     const int i = blk * kBlock + 8 * lane;
-    uint64_t above = 0, all = 0;  // all: of top-k's head but what is listed
+    uint64_t above = 0, all = 0;
     if (i < n) {
       float v[8];
       load8(z, vec, n, i, v);
@@ -498,13 +567,11 @@ __device__ __forceinline__ void sum_masses(FilterShared& s, const FixScale& scal
       for (int q = 0; q < 8; ++q) {
         float r;
         const uint32_t steps = fix_steps<kBig>(scale, v[q], r);
-        const int b = bn.bin(steps);
-        const bool in_list = (any_band && static_cast<uint32_t>(b - bin_lo) <= band) || b == bin_k;
-        listed |= in_list ? 1u << q : 0u;
+        if ((kMass && band.has(steps)) || (kCutK && of_k.has(steps))) listed |= 1u << q;
         if (kMass) {
           const uint64_t w = fix_weight_at(scale, s.table, steps, r);
-          if (b < bin_lo) above += w;
-          if (!in_list && b < bin_k) all += w;
+          if (steps < band.lo) above += w;
+          if (!kCutK || steps < of_k.lo) all += w;
         }
       }
       while (listed) {
@@ -515,12 +582,12 @@ __device__ __forceinline__ void sum_masses(FilterShared& s, const FixScale& scal
         for (int t = 1; t < 8; ++t) x = q == t ? v[t] : x;
         if (!(x > -INFINITY)) continue;
         const int at = atomicAdd(&s.listed, 1);
-        if (at < kList) s.list[at] = entry_of(x, v0 + i + q);
+        if (at < kList) s.list[at] = en.of(x, v0 + i + q);
       }
     }
     if (kMass) {
-      sum_r += all - above;
-      above = warp_sum(above);
+      sum_all += all;
+      above = warp_sum48(above);  // (eight weights of at most 2^44 a lane)
       if (lane == 0) {
         block_mass[blk] = above;
         sum_a += above;
@@ -660,6 +727,7 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
     }
     return;  // the whole cluster does; nobody's memory is in use
   }
+  const Entries<E> en{32 - __clz(V - 1)};
   FixScale scale;
   scale.init(zmax, s.c_hi, s.c_lo, a.fix_bits);
 
@@ -728,8 +796,8 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
           lo_sum += lo[i];
           hi_sum += hi[i];
         }
-        uint64_t lo_at = block_scan(s.red, lo_sum, lo_all);
-        uint64_t hi_at = block_scan(s.red, hi_sum, hi_all);
+        uint64_t lo_at, hi_at;
+        block_scan2(s.red, lo_sum, hi_sum, lo_at, hi_at, lo_all, hi_all);
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
           if (c[i]) {
@@ -762,23 +830,29 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
     // the exact masses above the band, by blocks, and of the rest of top-k's
     // head but the band and bin_k; what is in these two is listed
     FilterShared* first_cta = cluster.map_shared_rank(&s, 0);
-    uint64_t sum_a = 0, sum_r = 0;
+    uint64_t sum_a = 0, sum_all = 0;
     // (the bins are those of pass 2: the same steps)
-    const auto masses = [&](auto big, auto mass) {
-      sum_masses<decltype(big)::value, decltype(mass)::value>(
-          s, scale, bn, z, vec, v0, n, bin_k, bin_lo, bin_hi, block_mass, sum_a, sum_r);
+    const Steps of_k = bn.steps(bin_k, bin_k), band = bn.steps(bin_lo, bin_hi);
+    const auto masses = [&](auto big, auto mass, auto by_k) {
+      sum_masses<decltype(big)::value, decltype(mass)::value, decltype(by_k)::value>(
+          s, scale, en, z, vec, v0, n, of_k, band, block_mass, sum_a, sum_all);
     };
     using Yes = std::integral_constant<bool, true>;
     using No = std::integral_constant<bool, false>;
-    if (scale.big) want_p ? masses(Yes(), Yes()) : masses(Yes(), No());
-    else want_p ? masses(No(), Yes()) : masses(No(), No());
+    if (scale.big) {
+      if (!want_p) masses(Yes(), No(), Yes());
+      else cut_k ? masses(Yes(), Yes(), Yes()) : masses(Yes(), Yes(), No());
+    } else {
+      if (!want_p) masses(No(), No(), Yes());
+      else cut_k ? masses(No(), Yes(), Yes()) : masses(No(), Yes(), No());
+    }
     if (want_p) {
       sum_a = block_sum(s, sum_a);
-      sum_r = block_sum(s, sum_r);
+      sum_all = block_sum(s, sum_all);
       if (threadIdx.x < static_cast<unsigned>(parts)) {
         FilterShared* o = cluster.map_shared_rank(&s, threadIdx.x);
         o->part_a[part] = sum_a;
-        o->part_b[part] = sum_r;
+        o->part_b[part] = sum_all;
       }
     }
     if (!lead) {
@@ -800,35 +874,39 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
           // (the list holds whole bins: those above bin_k are among above_k)
           int over = 0;
           for (int i = threadIdx.x; i < listed; i += kFilterThreads)
-            over += bn.bin(scale, entry_value(s.list[i])) < bin_k;
+            over += bn.bin(scale, en.value(s.list[i])) < bin_k;
           const uint64_t over_all = block_sum(s, over);
-          least = select_list(s, scale, false, listed, k - s.above_k + over_all);
+          least = select_list(s, scale, en, false, listed, k - s.above_k + over_all);
         }
         if (want_p) {
-          uint64_t x = 0;
-          for (int i = threadIdx.x; i < listed; i += kFilterThreads) {
-            const uint64_t e = s.list[i];
-            if (e >= least) x += fix_weight(scale, s.table, entry_value(e));
-          }
-          uint64_t total = block_sum(s, x), base = 0;
+          uint64_t total = 0, base = 0;
           for (int i = 0; i < parts; ++i) {
             base += s.part_a[i];
-            total += s.part_a[i] + s.part_b[i];
+            total += s.part_b[i];
           }
-          const uint64_t e = select_list(s, scale, true, listed, mass_target(total, pf) - base);
+          if (cut_k) {  // what of bin_k is in top-k's head
+            uint64_t x = 0;
+            for (int i = threadIdx.x; i < listed; i += kFilterThreads) {
+              const uint64_t e = s.list[i];
+              const float y = en.value(e);
+              if (e >= least && bn.bin(scale, y) == bin_k) x += fix_weight(scale, s.table, y);
+            }
+            total += block_sum(s, x);
+          }
+          const uint64_t e = select_list(s, scale, en, true, listed, mass_target(total, pf) - base);
           least = e > least ? e : least;
           for (int i = threadIdx.x; i < listed; i += kFilterThreads) {
             const uint64_t e = s.list[i];
             if (e < least) continue;
-            const int blk = entry_index(e) / kBlock, per = a.per * (kKeepChunk / kBlock);
+            const int blk = en.index(e) / kBlock, per = a.per * (kKeepChunk / kBlock);
             atomicAdd(reinterpret_cast<unsigned long long*>(
                           cluster.map_shared_rank(block_mass, blk / per) + blk % per),
-                      static_cast<unsigned long long>(fix_weight(scale, s.table, entry_value(e))));
+                      static_cast<unsigned long long>(fix_weight(scale, s.table, en.value(e))));
           }
         }
         if (threadIdx.x == 0) {
-          s.cut_t = listed > 0 ? entry_value(least) : -INFINITY;  // nothing listed: no cut
-          s.cut_last = listed > 0 ? entry_index(least) : -1;
+          s.cut_t = listed > 0 ? en.value(least) : -INFINITY;  // nothing listed: no cut
+          s.cut_last = listed > 0 ? en.index(least) : -1;
         }
         __syncthreads();
       }
@@ -1012,7 +1090,14 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
   if (r < before || r - before >= mine) return;  // (nobody writes to this CTA any more)
   r -= before;
 
-  // ---- the block, then the column
+  // ---- the log-sum-exp; meanwhile the block, then the column
+  if (warp == 1) {
+    const float2 st = keep_merge(states, a.chunks, c);
+    if (lane == 0) {
+      s.redf[1] = st.x;
+      s.redf[2] = st.y;
+    }
+  }
   if (warp == 0) {
     const int blocks = (n + kBlock - 1) / kBlock;
     uint64_t at = 0;
@@ -1050,12 +1135,9 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
     s.redf[0] = x;
   }
   __syncthreads();
-  if (warp == 0) {
-    const float2 st = keep_merge(states, a.chunks, c);
-    if (lane == 0) {
-      a.logprob[row] = keep_logprob_of(s.redf[0], st, tau);
-      if (a.kept) a.kept[row] = kept_all;
-    }
+  if (threadIdx.x == 0) {
+    a.logprob[row] = keep_logprob_of(s.redf[0], make_float2(s.redf[1], s.redf[2]), tau);
+    if (a.kept) a.kept[row] = kept_all;
   }
 }
 

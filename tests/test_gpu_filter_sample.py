@@ -144,6 +144,27 @@ def test_wide_vocabulary(rz, V, dtype):
     assert ((got - (1 - p_tok)).abs() <= eps).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("V", [8193, 9217, 16385, 40003, 151936, 700001])
+def test_few_rows_as_in_a_large_batch(rz, V, dtype):
+    """One to four rows, which more CTAs share, give what they give among sixty-four."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(14)
+    T = 64
+    z = (2 * torch.randn(T, V, generator=g, device=DEV)).to(DT[dtype])
+    f = [FILTERS[r % len(FILTERS)] for r in range(T)]
+    temp = _t([[1.0, 0.7, 0.0][r % 3] for r in range(T)])
+    k, p, mp = (_t([x[i] for x in f], d) for i, d in
+                enumerate([torch.int32, torch.float32, torch.float32]))
+    u = torch.rand(T, generator=g, device=DEV)
+    all_ = _run(rz, z, temp, k, p, mp, u)
+    for lo, n in [(0, 1), (1, 1), (2, 2), (4, 3), (7, 4), (11, 4), (15, 6)]:
+        at = slice(lo, lo + n)
+        few = _run(rz, z[at], temp[at], k[at], p[at], mp[at], u[at])
+        for x, y in zip(few, all_):
+            assert torch.equal(x, y[at])
+
+
 def test_no_filters_at_all_and_row_strides(rz):
     g = torch.Generator(device=DEV)
     g.manual_seed(5)

@@ -681,11 +681,8 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
       mn = fminf(mn, x > -INFINITY ? x : mn);
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-  }
+  asm volatile("redux.sync.max.NaN.f32 %0, %0, 0xffffffff;" : "+f"(mx));
+  mn = -warp_max(-mn);
   if (lane == 0) {
     s.redf[warp] = mx;
     s.redf[kFilterWarps + warp] = mn;
@@ -1009,8 +1006,7 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
     float2 st = make_float2(-INFINITY, 0.f);
     if (__any_sync(0xffffffffu, bits != 0)) {
       // what is kept is a head of the order: the chunk's maximum is
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      m = warp_max(m);
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
       int top = 0;
 #pragma unroll
@@ -1057,10 +1053,8 @@ __global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
       }
       float r = __fadd_rn(__fadd_rn(acc[0], acc[1]), __fadd_rn(acc[2], acc[3]));
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, o));
-        top += __shfl_xor_sync(0xffffffffu, top, o);
-      }
+      for (int o = 16; o > 0; o >>= 1) r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, o));
+      top = __reduce_add_sync(0xffffffffu, top);
       st = make_float2(m, __fadd_rn(r, static_cast<float>(top - 1)));
     } else if (lane < kKeepSteps) {
       block_mass[ch * kKeepSteps + lane] = 0;

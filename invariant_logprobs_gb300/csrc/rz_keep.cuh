@@ -75,6 +75,13 @@ __device__ __forceinline__ void load8(const E* row, bool vec, int V, int col, fl
   }
 }
 
+// The warp's maximum in one instruction (a butterfly takes ten, in a chain).
+__device__ __forceinline__ float warp_max(float x) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
+}
+
 // Row temperature: NaN if out of range (0 counts as 1; so does none).
 __device__ __forceinline__ float row_tau(const float* temperature, long long row) {
   if (!temperature) return 1.f;
@@ -103,8 +110,7 @@ __device__ __forceinline__ float2 keep_fold(const E* row, bool vec, int V, int c
   for (int j = 0; j < kKeepSteps; ++j)
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = fmaxf(m, v[j][i]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  m = warp_max(m);
   const float ref = m == -INFINITY ? 0.f : m;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   int top = 0;
@@ -119,10 +125,8 @@ __device__ __forceinline__ float2 keep_fold(const E* row, bool vec, int V, int c
     }
   float r = __fadd_rn(__fadd_rn(acc[0], acc[1]), __fadd_rn(acc[2], acc[3]));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, o));
-    top += __shfl_xor_sync(0xffffffffu, top, o);
-  }
+  for (int o = 16; o > 0; o >>= 1) r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, o));
+  top = __reduce_add_sync(0xffffffffu, top);
   // an empty chunk: 0 (NaN if it holds NaNs)
   return make_float2(m, m == -INFINITY ? r : __fadd_rn(r, static_cast<float>(top - 1)));
 }
@@ -146,8 +150,7 @@ __device__ __forceinline__ float2 keep_fold_few(const E* row, int chunk, float c
   }
 #pragma unroll
   for (int k = 0; k < kKeepFew; ++k) m = fmaxf(m, v[k]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  m = warp_max(m);
   const float ref = m == -INFINITY ? 0.f : m;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   int top = 0;
@@ -162,10 +165,8 @@ __device__ __forceinline__ float2 keep_fold_few(const E* row, int chunk, float c
   }
   float r = __fadd_rn(__fadd_rn(acc[0], acc[1]), __fadd_rn(acc[2], acc[3]));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, o));
-    top += __shfl_xor_sync(0xffffffffu, top, o);
-  }
+  for (int o = 16; o > 0; o >>= 1) r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, o));
+  top = __reduce_add_sync(0xffffffffu, top);
   return make_float2(m, m == -INFINITY ? r : __fadd_rn(r, static_cast<float>(top - 1)));
 }
 
@@ -175,8 +176,7 @@ __device__ __forceinline__ float2 keep_merge(const float2* st, int n, float c) {
   const int lane = threadIdx.x & 31;
   float M = -INFINITY;
   for (int i = lane; i < n; i += 32) M = fmaxf(M, st[i].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  M = warp_max(M);
   const float ref = M == -INFINITY ? 0.f : M;
   float r = 0.f;
   int top = 0;
@@ -191,10 +191,8 @@ __device__ __forceinline__ float2 keep_merge(const float2* st, int n, float c) {
     }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, o));
-    top += __shfl_xor_sync(0xffffffffu, top, o);
-  }
+  for (int o = 16; o > 0; o >>= 1) r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, o));
+  top = __reduce_add_sync(0xffffffffu, top);
   return make_float2(M, M == -INFINITY ? r : __fadd_rn(r, static_cast<float>(top - 1)));
 }
 

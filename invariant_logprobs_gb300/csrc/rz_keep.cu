@@ -26,7 +26,21 @@ constexpr int kKeepThreads = 256;
 constexpr int kKeepWarps = kKeepThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaskAhead = 4;
-constexpr int kFwdCtas = 4, kBwdCtas = 32;  // CTAs wanted for each SM
+constexpr int kBwdCtas = 32;  // CTAs wanted for each SM
+
+// CTAs that share an SM in the forward pass, which is the registers a thread
+// has.  A dense row keeps one chunk's loads under way behind the fold of another:
+// 1,024 x 151,936 fp32 at 2 CTAs 120 us, 3: 128, 4 (spilled) 149, without the
+// loads ahead 145; bf16 at 4: 77, 3: 83, 2: 95, without 132.  Behind a mask few
+// chunks hold much and what counts is the number of loads under way: 4,096
+// bf16 rows with some tens kept at 8 CTAs 79 us, 6: 83, 4: 96; with half of the
+// tokens kept (1,024 rows) 121, 131, 145.  fp32's chunk takes twice the
+// registers: half kept at 4 CTAs 159 us, 5: 169, 6: 177, some hundreds kept 69,
+// 67, 69.
+template <class E>
+constexpr int fwd_ctas(bool masked) {
+  return sizeof(E) == 4 ? (masked ? 4 : 2) : (masked ? 8 : 4);
+}
 
 struct KeepArgs {
   const void* logits;
@@ -67,8 +81,9 @@ __device__ __forceinline__ bool mask_has(const uint32_t* words, int v) {
   return !words || ((words[v >> 5] >> (v & 31)) & 1u);
 }
 
-template <class E>
-__global__ void __launch_bounds__(kKeepThreads, 4) keep_logprob_kernel(const KeepArgs a) {
+template <class E, bool kMasked>
+__global__ void __launch_bounds__(kKeepThreads, fwd_ctas<E>(kMasked))
+    keep_logprob_kernel(const KeepArgs a) {
   extern __shared__ float2 states[];  // of the whole row, in the first CTA of the cluster; a list
   __shared__ int n_list;
   cg::cluster_group cluster = cg::this_cluster();
@@ -78,16 +93,16 @@ __global__ void __launch_bounds__(kKeepThreads, 4) keep_logprob_kernel(const Kee
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const E* z = static_cast<const E*>(a.logits) + row * a.ld;
   const bool vec = row_aligned(z);
-  const uint32_t* mask = a.keep ? a.keep + row * a.words : nullptr;
+  const uint32_t* mask = kMasked ? a.keep + row * a.words : nullptr;
   const float tau = row_tau(a.temperature, row);
   const float c = keep_scale(tau);
   float2* dst = cluster.map_shared_rank(states, 0);
   if (parts > 1) cluster.sync();  // every CTA of the cluster runs before its memory is written
-  // The chunks with something kept, from the mask, several loads of it under
-  // way together; most of a filtered row's hold nothing, and are done.
-  uint16_t* list = reinterpret_cast<uint16_t*>(states + a.chunks);
   const int step = parts * kKeepWarps;
-  if (mask) {
+  if (kMasked) {
+    // The chunks with something kept, from the mask, several loads of it under
+    // way together; most of a filtered row's hold nothing, and are done.
+    uint16_t* list = reinterpret_cast<uint16_t*>(states + a.chunks);
     if (threadIdx.x == 0) n_list = 0;
     __syncthreads();
     for (int ch0 = part * kKeepWarps + warp; ch0 < a.chunks; ch0 += kMaskAhead * step) {
@@ -105,17 +120,34 @@ __global__ void __launch_bounds__(kKeepThreads, 4) keep_logprob_kernel(const Kee
       }
     }
     __syncthreads();
-  }
-  const int n = mask ? n_list : (a.chunks - part * kKeepWarps + step - 1) / step * kKeepWarps;
+    const int n = n_list;
 #pragma unroll 1
-  for (int i = warp; i < n; i += kKeepWarps) {
-    const int ch = mask ? list[i] : part * kKeepWarps + i % kKeepWarps + i / kKeepWarps * step;
-    if (ch >= a.chunks) break;
-    const uint32_t bits = lane_bits(mask_word(mask, a.V, ch));
-    const float2 st = __any_sync(0xffffffffu, __popc(bits) > kKeepFew)
-                          ? keep_fold(z, vec, a.V, ch, c, bits)
-                          : keep_fold_few(z, ch, c, bits);
-    if (lane == 0) dst[ch] = st;
+    for (int i = warp; i < n; i += kKeepWarps) {
+      const int ch = list[i];
+      const uint32_t bits = lane_bits(mask_word(mask, a.V, ch));
+      const float2 st = __any_sync(0xffffffffu, __popc(bits) > kKeepFew)
+                            ? keep_fold(z, vec, a.V, ch, c, bits)
+                            : keep_fold_few(z, ch, c, bits);
+      if (lane == 0) dst[ch] = st;
+    }
+  } else {
+    // Every chunk, the next one's loads under way while one is folded.
+    const int whole = vec ? a.V / kKeepChunk : 0;
+    KeepRaw<E> raw;
+    int ch = part * kKeepWarps + warp;
+    if (ch < whole) raw.load(z, ch);
+#pragma unroll 2
+    for (; ch < whole; ch += step) {
+      const KeepRaw<E> now = raw;
+      if (ch + step < whole) raw.load(z, ch + step);
+      const float2 st = now.fold(c);
+      if (lane == 0) dst[ch] = st;
+    }
+#pragma unroll 1
+    for (; ch < a.chunks; ch += step) {
+      const float2 st = keep_fold(z, vec, a.V, ch, c, lane_bits(mask_word(nullptr, a.V, ch)));
+      if (lane == 0) dst[ch] = st;
+    }
   }
   if (parts > 1) cluster.sync();
   else __syncthreads();
@@ -228,17 +260,17 @@ __global__ void __launch_bounds__(kKeepThreads) keep_logprob_bwd_kernel(const Ke
   }
 }
 
-template <class E>
-cudaError_t launch_fwd(const KeepArgs& a, cudaStream_t st) {
+template <class E, bool kMasked>
+cudaError_t launch_fwd_as(const KeepArgs& a, cudaStream_t st) {
   // One row to a CTA while that fills the GPU twice; else its chunks over a
   // cluster of up to eight CTAs, whose states meet in the first one's memory.
   int parts = 1;
-  while (parts < kMaxCluster && a.T * parts < kFwdCtas * num_sms() &&
+  while (parts < kMaxCluster && a.T * parts < fwd_ctas<E>(kMasked) * num_sms() &&
          parts * kKeepWarps < a.chunks)
     parts *= 2;
   const size_t smem = static_cast<size_t>(a.chunks) * (sizeof(float2) + sizeof(uint16_t));
   static SmemOnce once;
-  const cudaError_t e = once.set(keep_logprob_kernel<E>, 196608);
+  const cudaError_t e = once.set(keep_logprob_kernel<E, kMasked>, 196608);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(a.T * parts));
@@ -252,7 +284,12 @@ cudaError_t launch_fwd(const KeepArgs& a, cudaStream_t st) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, keep_logprob_kernel<E>, a);
+  return cudaLaunchKernelEx(&cfg, keep_logprob_kernel<E, kMasked>, a);
+}
+
+template <class E>
+cudaError_t launch_fwd(const KeepArgs& a, cudaStream_t st) {
+  return a.keep ? launch_fwd_as<E, true>(a, st) : launch_fwd_as<E, false>(a, st);
 }
 
 template <class E>

@@ -90,45 +90,86 @@ __device__ __forceinline__ float row_tau(const float* temperature, long long row
   return t >= 9.5367431640625e-07f && t <= 1048576.f ? t : __int_as_float(0x7fc00000);
 }
 
-// Fold of one chunk by one warp; bits: which of the lane's columns are kept, 8
-// for each step (none kept in a step: nothing of it is loaded).
-template <class E>
-__device__ __forceinline__ float2 keep_fold(const E* row, bool vec, int V, int chunk, float c,
-                                            uint32_t bits) {
-  const int col0 = chunk * kKeepChunk + 8 * (threadIdx.x & 31);
-  float v[kKeepSteps][8];
+// Fold of one chunk by one warp; get(j, v): the lane's columns of step j, -inf
+// where not kept (asked for twice).
+template <class Get>
+__device__ __forceinline__ float2 keep_fold_of(float c, const Get& get) {
   float m = -INFINITY;
 #pragma unroll
   for (int j = 0; j < kKeepSteps; ++j) {
-    const uint32_t b = (bits >> (8 * j)) & 255u;
-    if (b) load8(row, vec, V, col0 + 256 * j, v[j]);
+    float v[8];
+    get(j, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (!((b >> i) & 1u)) v[j][i] = -INFINITY;
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, v[i]);
   }
-#pragma unroll
-  for (int j = 0; j < kKeepSteps; ++j)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, v[j][i]);
   m = warp_max(m);
   const float ref = m == -INFINITY ? 0.f : m;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   int top = 0;
 #pragma unroll
-  for (int j = 0; j < kKeepSteps; ++j)
+  for (int j = 0; j < kKeepSteps; ++j) {
+    float v[8];
+    get(j, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float t = ex2_approx(__fmul_rn(__fsub_rn(v[j][i], ref), c));
-      const bool is_top = v[j][i] == m;
+      const float t = ex2_approx(__fmul_rn(__fsub_rn(v[i], ref), c));
+      const bool is_top = v[i] == m;
       acc[i & 3] = __fadd_rn(acc[i & 3], is_top ? 0.f : t);
       top += is_top;
     }
+  }
   float r = __fadd_rn(__fadd_rn(acc[0], acc[1]), __fadd_rn(acc[2], acc[3]));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, o));
   top = __reduce_add_sync(0xffffffffu, top);
   // an empty chunk: 0 (NaN if it holds NaNs)
   return make_float2(m, m == -INFINITY ? r : __fadd_rn(r, static_cast<float>(top - 1)));
+}
+
+// A chunk's columns as they lie in memory.
+template <class E>
+struct KeepRaw {
+  static constexpr int kVecs = sizeof(E) / 2;
+  uint4 q[kKeepSteps][kVecs];
+  // bits: which of the lane's columns are kept, 8 for each step (none kept in a
+  // step: nothing of it is loaded).  The chunk lies within V and is aligned.
+  __device__ __forceinline__ void load(const E* row, int chunk, uint32_t bits = ~0u) {
+    const uint4* p = reinterpret_cast<const uint4*>(
+        row + static_cast<long long>(chunk) * kKeepChunk + 8 * (threadIdx.x & 31));
+#pragma unroll
+    for (int j = 0; j < kKeepSteps; ++j)
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i)
+        q[j][i] = (bits >> (8 * j)) & 255u ? p[j * 32 * kVecs + i] : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ float2 fold(float c) const {
+    return keep_fold_of(c, [&](int j, float (&v)[8]) { unpack8(q[j], v, E()); });
+  }
+  __device__ __forceinline__ float2 fold(float c, uint32_t bits) const {
+    return keep_fold_of(c, [&](int j, float (&v)[8]) {
+      unpack8(q[j], v, E());
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = (bits >> (8 * j + i)) & 1u ? v[i] : -INFINITY;
+    });
+  }
+};
+
+// Any chunk of a row.
+template <class E>
+__device__ __forceinline__ float2 keep_fold(const E* row, bool vec, int V, int chunk, float c,
+                                            uint32_t bits) {
+  if (vec && (chunk + 1) * kKeepChunk <= V) {
+    KeepRaw<E> raw;
+    raw.load(row, chunk, bits);
+    return raw.fold(c, bits);
+  }
+  const int col0 = chunk * kKeepChunk + 8 * (threadIdx.x & 31);
+  return keep_fold_of(c, [&](int j, float (&v)[8]) {
+    const uint32_t b = (bits >> (8 * j)) & 255u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = (b >> i) & 1u ? to_f32(row[col0 + 256 * j + i]) : -INFINITY;
+  });
 }
 
 // The same for a chunk of which no lane keeps more than kKeepFew columns: those

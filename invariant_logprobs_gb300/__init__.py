@@ -12,6 +12,7 @@ Build the library with ``python -m invariant_logprobs_gb300.build`` (or
 """
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -53,6 +54,7 @@ RZ_OP_GROUP_DECODE_ATTN = 7
 
 _lib = None
 _torch_module = None
+_dtype_ids = {}  # torch dtype: RZ_DTYPE_*
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -139,6 +141,8 @@ def _torch():
     global _torch_module
     if _torch_module is None:
         import torch
+        _dtype_ids.update({torch.float32: RZ_DTYPE_F32, torch.bfloat16: RZ_DTYPE_BF16,
+                           torch.float16: RZ_DTYPE_F16})
         _torch_module = torch
     return _torch_module
 
@@ -169,10 +173,17 @@ def _check(name, status):
         raise RzError(name, status)
 
 
-def _need(t, dtype, name):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+def _need(t, dtype, name, shape=None):
+    """t: a contiguous CUDA tensor of dtype (and of the given shape).  (Every
+    check of a call counts: a small launch takes the host 3 us.)"""
+    try:
+        ok = t.dtype is dtype and t.is_cuda and t.is_contiguous()
+    except AttributeError:  # not a tensor
+        ok = False
+    if not ok:
         raise TypeError("%s must be a contiguous CUDA tensor of %s" % (name, dtype))
+    if shape is not None and t.shape != shape:
+        _shape(t, shape, name)
 
 
 def _out(t, dtype, name, shape=None, min_numel=1):
@@ -205,14 +216,13 @@ def _same_device(*ts):
     library launches on the current device's context."""
     dev = None
     for t in ts:
-        if t is None:
-            continue
-        d = t.device
-        if dev is None:
-            dev = d
-        elif d != dev:
-            devs = {str(x.device) for x in ts if x is not None}
-            raise ValueError("all tensors must be on one CUDA device, got %s" % sorted(devs))
+        if t is not None:
+            d = t.device
+            if dev is None:
+                dev = d
+            elif d != dev:
+                devs = {str(x.device) for x in ts if x is not None}
+                raise ValueError("all tensors must be on one CUDA device, got %s" % sorted(devs))
     if dev is not None:
         cur = _torch().cuda.current_device()
         if dev.type == "cuda" and dev.index is not None and dev.index != cur:
@@ -663,12 +673,12 @@ def rz_sample_logprob(H, W, seed, row_ids=None, tokens_out=None, logprob_out=Non
 # ------------------------------------------------------- rollouts of response groups
 def _dtype_id(t, name, allowed):
     torch = _torch()
-    ids = {torch.float32: RZ_DTYPE_F32, torch.bfloat16: RZ_DTYPE_BF16, torch.float16: RZ_DTYPE_F16}
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or ids.get(t.dtype) not in allowed:
-        names = {v: str(k) for k, v in ids.items()}
+    i = _dtype_ids.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if i not in allowed or not t.is_cuda:
+        names = {v: str(k) for k, v in _dtype_ids.items()}
         raise TypeError("%s must be a CUDA tensor of %s"
                         % (name, " or ".join(names[i] for i in allowed)))
-    return ids[t.dtype]
+    return i
 
 
 def _new(shape, dtype, device, stream):
@@ -684,22 +694,17 @@ def _new(shape, dtype, device, stream):
 def _rows(t, name):
     """[T, V] with contiguous rows; returns (dtype id, T, V, row stride)."""
     dt = _dtype_id(t, name, (RZ_DTYPE_F32, RZ_DTYPE_BF16, RZ_DTYPE_F16))
-    if t.dim() != 2 or t.shape[1] < 1:
-        raise ValueError("%s must have shape [T, V] with V >= 1, got %s" % (name, tuple(t.shape)))
-    T, V = t.shape
-    ld = t.stride(0) if T > 1 else V
-    if (t.stride(1) != 1 and V > 1) or ld < V:
+    shape = t.shape
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError("%s must have shape [T, V] with V >= 1, got %s" % (name, tuple(shape)))
+    T, V = shape
+    ld, inner = t.stride()
+    if T <= 1:
+        ld = V
+    if (inner != 1 and V > 1) or ld < V:
         raise ValueError("%s must have contiguous rows that do not overlap, got strides %s"
                          % (name, t.stride()))
     return dt, T, V, ld
-
-
-def _row_params(T, **tensors):
-    """Optional per-row parameters: contiguous CUDA tensors [T] of a dtype."""
-    for name, (t, dtype) in tensors.items():
-        if t is not None:
-            _need(t, dtype, name)
-            _shape(t, (T,), name)
 
 
 def rz_page_tables(lens, new_lens, free_pages, page_size, table, n_slots, slots_out=None,
@@ -710,20 +715,25 @@ def rz_page_tables(lens, new_lens, free_pages, page_size, table, n_slots, slots_
     Returns (slots [n_slots] int64, cu [B+1] int64, used [1] int32)."""
     torch = _torch()
     lib = load()
-    _need(lens, torch.int32, "lens")
-    _need(new_lens, torch.int32, "new_lens")
-    _need(free_pages, torch.int32, "free_pages")
-    _need(table, torch.int32, "table")
+    int32 = torch.int32
+    _need(lens, int32, "lens")
+    _need(new_lens, int32, "new_lens")
+    _need(free_pages, int32, "free_pages")
+    _need(table, int32, "table")
     if table.dim() != 2:
         raise ValueError("table must have shape [B, width], got %s" % (tuple(table.shape),))
     B, width = table.shape
     n_slots = int(n_slots)
     _shape(lens, (B,), "lens")
     _shape(new_lens, (B,), "new_lens")
-    _out(slots_out, torch.int64, "slots_out", (n_slots,))
-    _out(cu_out, torch.int64, "cu_out", (B + 1,))
-    _out(used_out, torch.int32, "used_out")
-    _out(err_flag, torch.int32, "err_flag")
+    if slots_out is not None:
+        _out(slots_out, torch.int64, "slots_out", (n_slots,))
+    if cu_out is not None:
+        _out(cu_out, torch.int64, "cu_out", (B + 1,))
+    if used_out is not None:
+        _out(used_out, int32, "used_out")
+    if err_flag is not None:
+        _out(err_flag, int32, "err_flag")
     _same_device(lens, new_lens, free_pages, table, slots_out, cu_out, used_out, err_flag)
     strm = _stream(stream)
     if n_slots < 0:
@@ -735,11 +745,18 @@ def rz_page_tables(lens, new_lens, free_pages, page_size, table, n_slots, slots_
         cu_out = _new(B + 1, torch.int64, dev, stream)
     if used_out is None:
         used_out = _new(1, torch.int32, dev, stream)
-    st = lib.rz_page_tables(_ptr(lens), _ptr(new_lens), B, _ptr(free_pages), free_pages.numel(),
-                            int(page_size), _ptr(table), width, _ptr(slots_out), n_slots,
-                            _ptr(cu_out), _ptr(used_out), _ptr(err_flag), strm)
-    _check("rz_page_tables", st)
+    st = lib.rz_page_tables(lens.data_ptr(), new_lens.data_ptr(), B, free_pages.data_ptr(),
+                            free_pages.numel(), int(page_size), table.data_ptr(), width,
+                            slots_out.data_ptr(), n_slots, cu_out.data_ptr(),
+                            used_out.data_ptr(), _ptr(err_flag), strm)
+    if st != RZ_OK:
+        raise RzError("rz_page_tables", st)
     return slots_out, cu_out, used_out
+
+
+@functools.lru_cache(maxsize=1024)
+def _attn_ws(B, D, Hq, P):
+    return max(workspace_size(RZ_OP_GROUP_DECODE_ATTN, B, D, Hq, P), 256)
 
 
 def rz_group_decode_attn(q, k_cache, v_cache, table, lens, prefix_table=None, prefix_lens=None,
@@ -760,9 +777,11 @@ def rz_group_decode_attn(q, k_cache, v_cache, table, lens, prefix_table=None, pr
         if t.dim() != 4 or t.shape[1] < 1:
             raise ValueError("%s must have shape [n_pages, page, Hkv, D], got %s"
                              % (name, tuple(t.shape)))
-    n_pages, page, Hkv, _ = k_cache.shape
-    _shape(k_cache, (n_pages, page, Hkv, D), "k_cache")
-    _shape(v_cache, (n_pages, page, Hkv, D), "v_cache")
+    n_pages, page, Hkv, Dk = k_cache.shape
+    if Dk != D:
+        _shape(k_cache, (n_pages, page, Hkv, D), "k_cache")
+    if v_cache.shape != k_cache.shape:
+        _shape(v_cache, (n_pages, page, Hkv, D), "v_cache")
     qst, kst, vst = q.stride(), k_cache.stride(), v_cache.stride()
     for st, name in ((qst, "q"), (kst, "k_cache"), (vst, "v_cache")):
         if st[-1] != 1 and D > 1:
@@ -770,51 +789,60 @@ def rz_group_decode_attn(q, k_cache, v_cache, table, lens, prefix_table=None, pr
                              % (name, st))
         if min(st) < 0:
             raise ValueError("%s has a negative stride" % name)
-    _need(table, torch.int32, "table")
-    _need(lens, torch.int32, "lens")
+    int32 = torch.int32
+    _need(table, int32, "table")
+    _need(lens, int32, "lens")
     if table.dim() != 2:
         raise ValueError("table must have shape [B, width], got %s" % (tuple(table.shape),))
-    _shape(table, (B, table.shape[1]), "table")
+    rows, width = table.shape
+    if rows != B:
+        _shape(table, (B, width), "table")
     _shape(lens, (B,), "lens")
-    group = (prefix_table, prefix_lens, cu_group)
-    if any(t is None for t in group) != all(t is None for t in group):
-        raise TypeError("prefix_table, prefix_lens and cu_group come together")
     P, prefix_width = 0, 0
-    if prefix_table is not None:
-        _need(prefix_table, torch.int32, "prefix_table")
-        _need(prefix_lens, torch.int32, "prefix_lens")
-        _need(cu_group, torch.int32, "cu_group")
+    if prefix_table is not None and prefix_lens is not None and cu_group is not None:
+        _need(prefix_table, int32, "prefix_table")
+        _need(prefix_lens, int32, "prefix_lens")
+        _need(cu_group, int32, "cu_group")
         if prefix_table.dim() != 2:
             raise ValueError("prefix_table must have shape [P, width], got %s"
                              % (tuple(prefix_table.shape),))
         P, prefix_width = prefix_table.shape
         _shape(prefix_lens, (P,), "prefix_lens")
         _shape(cu_group, (P + 1,), "cu_group")
-    _out(out, q.dtype, "out", (B, Hq, D))
-    _out(lse_out, torch.float32, "lse_out", (B, Hq))
-    _out(err_flag, torch.int32, "err_flag")
+    elif not (prefix_table is None and prefix_lens is None and cu_group is None):
+        raise TypeError("prefix_table, prefix_lens and cu_group come together")
+    if out is not None:
+        _out(out, q.dtype, "out", (B, Hq, D))
+    if lse_out is not None:
+        _out(lse_out, torch.float32, "lse_out", (B, Hq))
+    if err_flag is not None:
+        _out(err_flag, int32, "err_flag")
     _same_device(q, k_cache, v_cache, table, lens, prefix_table, prefix_lens, cu_group, out,
                  lse_out, ws, err_flag)
     strm = _stream(stream)
+    dev = q.device
     if ws is None:
-        n = workspace_size(RZ_OP_GROUP_DECODE_ATTN, B, D, Hq, P)
-        ws = _new(max(n, 256), torch.uint8, q.device, stream)
-    ws_bytes = _ws_bytes(ws)
+        ws_bytes = _attn_ws(B, D, Hq, P)
+        ws = _new(ws_bytes, torch.uint8, dev, stream)
+    else:
+        ws_bytes = _ws_bytes(ws)
     if out is None:
-        out = _new((B, Hq, D), q.dtype, q.device, stream)
+        out = _new((B, Hq, D), q.dtype, dev, stream)
     if lse_out is None:
-        lse_out = _new((B, Hq), torch.float32, q.device, stream)
+        lse_out = _new((B, Hq), torch.float32, dev, stream)
     # strides of axes that hold one element mean nothing: give them as 0
     qs = _I64x2(qst[0] if B > 1 else 0, qst[1] if Hq > 1 else 0)
     many = (n_pages > 1, page > 1, Hkv > 1)
     kvs = _I64x6(*[st[i] if many[i] else 0 for st in (kst, vst) for i in range(3)])
-    st = lib.rz_group_decode_attn(_ptr(q), qs, _ptr(k_cache), _ptr(v_cache), kvs, n_pages, page,
-                                  _ptr(prefix_table), prefix_width, _ptr(prefix_lens),
-                                  _ptr(cu_group), P, _ptr(table), table.shape[1], _ptr(lens), B,
-                                  Hq, Hkv, D, dt, float(D ** -0.5 if scale is None else scale),
-                                  _ptr(out), _ptr(lse_out), _ptr(ws), ws_bytes, _ptr(err_flag),
+    st = lib.rz_group_decode_attn(q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), kvs,
+                                  n_pages, page, _ptr(prefix_table), prefix_width,
+                                  _ptr(prefix_lens), _ptr(cu_group), P, table.data_ptr(), width,
+                                  lens.data_ptr(), B, Hq, Hkv, D, dt,
+                                  float(D ** -0.5 if scale is None else scale), out.data_ptr(),
+                                  lse_out.data_ptr(), ws.data_ptr(), ws_bytes, _ptr(err_flag),
                                   strm)
-    _check("rz_group_decode_attn", st)
+    if st != RZ_OK:
+        raise RzError("rz_group_decode_attn", st)
     return out, lse_out
 
 
@@ -829,17 +857,27 @@ def rz_filter_sample(logits, uniform, temperature=None, top_k=None, top_p=None, 
     torch = _torch()
     lib = load()
     dt, T, V, ld = _rows(logits, "logits")
-    if uniform is None:
-        raise TypeError("uniform must be a contiguous CUDA tensor of torch.float32")
-    _row_params(T, uniform=(uniform, torch.float32), temperature=(temperature, torch.float32),
-                top_k=(top_k, torch.int32), top_p=(top_p, torch.float32),
-                min_p=(min_p, torch.float32))
+    int32, float32, row = torch.int32, torch.float32, (T,)
+    _need(uniform, float32, "uniform", row)
+    if temperature is not None:
+        _need(temperature, float32, "temperature", row)
+    if top_k is not None:
+        _need(top_k, int32, "top_k", row)
+    if top_p is not None:
+        _need(top_p, float32, "top_p", row)
+    if min_p is not None:
+        _need(min_p, float32, "min_p", row)
     words = (V + 31) // 32
-    _out(tokens_out, torch.int32, "tokens_out", (T,))
-    _out(logprob_out, torch.float32, "logprob_out", (T,))
-    _out(kept_out, torch.int32, "kept_out", (T,))
-    _out(keep_out, torch.int32, "keep_out", (T, words))
-    _out(err_flag, torch.int32, "err_flag")
+    if tokens_out is not None:
+        _need(tokens_out, int32, "tokens_out", row)
+    if logprob_out is not None:
+        _need(logprob_out, float32, "logprob_out", row)
+    if kept_out is not None:
+        _need(kept_out, int32, "kept_out", row)
+    if keep_out is not None:
+        _need(keep_out, int32, "keep_out", (T, words))
+    if err_flag is not None:
+        _out(err_flag, int32, "err_flag")
     _same_device(logits, uniform, temperature, top_k, top_p, min_p, tokens_out, logprob_out,
                  kept_out, keep_out, err_flag)
     strm = _stream(stream)
@@ -852,23 +890,23 @@ def rz_filter_sample(logits, uniform, temperature=None, top_k=None, top_p=None, 
         kept_out = _new(T, torch.int32, dev, stream)
     if keep_out is None and want_keep:
         keep_out = _new((T, words), torch.int32, dev, stream)
-    st = lib.rz_filter_sample(_ptr(logits), ld, dt, T, V, _ptr(temperature), _ptr(top_k),
-                              _ptr(top_p), _ptr(min_p), _ptr(uniform), _ptr(tokens_out),
-                              _ptr(logprob_out), _ptr(kept_out), _ptr(keep_out), _ptr(err_flag),
-                              strm)
-    _check("rz_filter_sample", st)
+    st = lib.rz_filter_sample(logits.data_ptr(), ld, dt, T, V, _ptr(temperature), _ptr(top_k),
+                              _ptr(top_p), _ptr(min_p), uniform.data_ptr(),
+                              tokens_out.data_ptr(), logprob_out.data_ptr(), kept_out.data_ptr(),
+                              _ptr(keep_out), _ptr(err_flag), strm)
+    if st != RZ_OK:
+        raise RzError("rz_filter_sample", st)
     return tokens_out, logprob_out, kept_out, keep_out
 
 
 def _keep_rows(logits, tokens, keep, temperature):
     torch = _torch()
     dt, T, V, ld = _rows(logits, "logits")
-    _need(tokens, torch.int32, "tokens")
-    _shape(tokens, (T,), "tokens")
-    _row_params(T, temperature=(temperature, torch.float32))
+    _need(tokens, torch.int32, "tokens", (T,))
+    if temperature is not None:
+        _need(temperature, torch.float32, "temperature", (T,))
     if keep is not None:
-        _need(keep, torch.int32, "keep")
-        _shape(keep, (T, (V + 31) // 32), "keep")
+        _need(keep, torch.int32, "keep", (T, (V + 31) // 32))
     return dt, T, V, ld
 
 
@@ -880,18 +918,24 @@ def rz_keep_logprob(logits, tokens, keep=None, temperature=None, logprob_out=Non
     torch = _torch()
     lib = load()
     dt, T, V, ld = _keep_rows(logits, tokens, keep, temperature)
-    _out(logprob_out, torch.float32, "logprob_out", (T,))
-    _out(lse_out, torch.float32, "lse_out", (T,))
-    _out(err_flag, torch.int32, "err_flag")
+    float32 = torch.float32
+    if logprob_out is not None:
+        _need(logprob_out, float32, "logprob_out", (T,))
+    if lse_out is not None:
+        _need(lse_out, float32, "lse_out", (T,))
+    if err_flag is not None:
+        _out(err_flag, torch.int32, "err_flag")
     _same_device(logits, tokens, keep, temperature, logprob_out, lse_out, err_flag)
     strm = _stream(stream)
     if logprob_out is None:
-        logprob_out = _new(T, torch.float32, logits.device, stream)
+        logprob_out = _new(T, float32, logits.device, stream)
     if lse_out is None:
-        lse_out = _new(T, torch.float32, logits.device, stream)
-    st = lib.rz_keep_logprob(_ptr(logits), ld, dt, T, V, _ptr(keep), _ptr(temperature),
-                             _ptr(tokens), _ptr(logprob_out), _ptr(lse_out), _ptr(err_flag), strm)
-    _check("rz_keep_logprob", st)
+        lse_out = _new(T, float32, logits.device, stream)
+    st = lib.rz_keep_logprob(logits.data_ptr(), ld, dt, T, V, _ptr(keep), _ptr(temperature),
+                             tokens.data_ptr(), logprob_out.data_ptr(), lse_out.data_ptr(),
+                             _ptr(err_flag), strm)
+    if st != RZ_OK:
+        raise RzError("rz_keep_logprob", st)
     return logprob_out, lse_out
 
 
@@ -903,25 +947,25 @@ def rz_keep_logprob_bwd(logits, tokens, lse, dlogprob, keep=None, temperature=No
     torch = _torch()
     lib = load()
     dt, T, V, ld = _keep_rows(logits, tokens, keep, temperature)
-    _need(lse, torch.float32, "lse")
-    _shape(lse, (T,), "lse")
-    _need(dlogprob, torch.float32, "dlogprob")
-    _shape(dlogprob, (T,), "dlogprob")
+    _need(lse, torch.float32, "lse", (T,))
+    _need(dlogprob, torch.float32, "dlogprob", (T,))
     ldd = V
     if dlogits_out is not None:
         got, _, _, ldd = _rows(dlogits_out, "dlogits_out")
         _shape(dlogits_out, (T, V), "dlogits_out")
         if got != dt:
             raise TypeError("dlogits_out must have the dtype of logits, %s" % logits.dtype)
-    _out(err_flag, torch.int32, "err_flag")
+    if err_flag is not None:
+        _out(err_flag, torch.int32, "err_flag")
     _same_device(logits, tokens, lse, dlogprob, keep, temperature, dlogits_out, err_flag)
     strm = _stream(stream)
     if dlogits_out is None:
         dlogits_out = _new((T, V), logits.dtype, logits.device, stream)
-    st = lib.rz_keep_logprob_bwd(_ptr(logits), ld, dt, T, V, _ptr(keep), _ptr(temperature),
-                                 _ptr(tokens), _ptr(lse), _ptr(dlogprob), _ptr(dlogits_out), ldd,
-                                 _ptr(err_flag), strm)
-    _check("rz_keep_logprob_bwd", st)
+    st = lib.rz_keep_logprob_bwd(logits.data_ptr(), ld, dt, T, V, _ptr(keep), _ptr(temperature),
+                                 tokens.data_ptr(), lse.data_ptr(), dlogprob.data_ptr(),
+                                 dlogits_out.data_ptr(), ldd, _ptr(err_flag), strm)
+    if st != RZ_OK:
+        raise RzError("rz_keep_logprob_bwd", st)
     return dlogits_out
 
 

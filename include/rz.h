@@ -442,6 +442,7 @@ RZ_API int rz_page_tables(const int32_t* lens, const int32_t* new_lens, int32_t 
  *     s_j = scale q . k_j,  lse = log sum_j e^(s_j),  out = sum_j e^(s_j - lse) v_j
  *   over the prefix tokens and the own tokens; query head h reads KV head
  *   h / (Hq / Hkv).  No token at all: out = 0, lse = -inf.
+ * A table of width 0 may be null.
  * A prefix's K and V are read once for its whole group (once per 128 query
  * rows of a KV head).  Products of the 16-bit inputs on the tensor cores,
  * scores, softmax statistics and the output's sums in fp32, the softmax terms
@@ -453,7 +454,8 @@ RZ_API int rz_page_tables(const int32_t* lens, const int32_t* new_lens, int32_t 
  * Lengths past a row's width or negative are cut, page ids outside
  * [0, n_pages) are skipped, a cu_group that is not 0 <= cu[0] <= ... <= B is
  * cut to it: RZ_DEVERR_PAGES / RZ_DEVERR_CU_SEQLENS, no access leaves the
- * arrays.  Results do not change from run to run.  Workspace:
+ * arrays.  Results do not change from run to run; with the batch the places
+ * where a row's tokens are split over the SMs do, and so its roundings.  Workspace:
  * rz_workspace_size(RZ_OP_GROUP_DECODE_ATTN, B, D, Hq, P).
  */
 RZ_API int rz_group_decode_attn(const void* q, const int64_t* q_stride, const void* k_cache,
@@ -488,13 +490,13 @@ RZ_API int rz_group_decode_attn(const void* q, const int64_t* q_stride, const vo
  *   (nullable: bit v % 32 of word v / 32 says that v was kept)
  * The sums behind every decision are 64-bit integers: weights
  * e^((z - max z)/tau) rounded to 2^-44 (V <= 2^18) with a relative error of
- * about 2^-35, added exactly.  So a row's result does not depend on its batch,
+ * about 2^-31, added exactly.  So a row's result does not depend on its batch,
  * and equals that of exact arithmetic but for borders that close.
  * logprob_out is bitwise what rz_keep_logprob gives for the same logits,
  * token, temperature and keep_out.
  * A row with a NaN, a +inf or no finite logit (RZ_DEVERR_LOGITS), or a
  * parameter out of its range (RZ_DEVERR_PARAM): token -1, log mu NaN, none kept.
- * T >= 0, 1 <= V <= 2^24.  No workspace.
+ * 0 <= T < 2^28, 1 <= V <= 2^24.  No workspace.
  */
 RZ_API int rz_filter_sample(const void* logits, int64_t ld, int32_t dtype, int64_t T, int32_t V,
                             const float* temperature, const int32_t* top_k, const float* top_p,
@@ -514,7 +516,8 @@ RZ_API int rz_filter_sample(const void* logits, int64_t ld, int32_t dtype, int64
  *   logprob_out [T] fp32         z_a / tau - lse; -inf for a token not kept
  * Nothing kept, or only -inf: lse = logprob = -inf.  A token outside [0, V)
  * gives NaN and RZ_DEVERR_TOKEN_RANGE, a temperature out of range NaN and
- * RZ_DEVERR_PARAM.  A row's result does not depend on its batch.  No workspace.
+ * RZ_DEVERR_PARAM.  A row's result does not depend on its batch.
+ * 0 <= T < 2^31 - 1, 1 <= V <= 2^24.  No workspace.
  */
 RZ_API int rz_keep_logprob(const void* logits, int64_t ld, int32_t dtype, int64_t T, int32_t V,
                            const uint32_t* keep, const float* temperature, const int32_t* tokens,
@@ -625,8 +628,10 @@ RZ_API size_t rz_noalloc_scratch_bytes(void);
                                    the scaling of H's rows by sigma_t */
 #define RZ_PROF_DH_GEMM      4  /* dH = dz W */
 #define RZ_PROF_DW_GEMM      5  /* dW = dz^T H, accumulated over chunks */
-#define RZ_PROF_LOGITS_ROWS  6  /* given-logits row kernel */
-#define RZ_PROF_SMALL        7  /* advantages, response factors, loss, D3, statistics */
+#define RZ_PROF_LOGITS_ROWS  6  /* given-logits row kernel; filtered sampling,
+                                   kept-set log-probability and its gradient */
+#define RZ_PROF_SMALL        7  /* advantages, response factors, loss, D3, statistics;
+                                   page tables, group decode attention */
 #define RZ_PROF_CLASSES      8
 RZ_API int rz_profile_begin(void);
 RZ_API int rz_profile_end(float* ms_out, int32_t* launches_out, int32_t n_classes);

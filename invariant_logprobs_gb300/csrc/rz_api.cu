@@ -20,9 +20,9 @@ namespace rz {
 
 // ------------------------------------------------------------------ device facts
 namespace {
-// SM count and compute capability of a device, looked up once (0: not yet).
+// SM count, L2 bytes and compute capability of a device, looked up once (0: not yet).
 struct DeviceFacts {
-  std::atomic<int> sms{0}, capability{0};
+  std::atomic<int> sms{0}, l2{0}, capability{0};
 };
 DeviceFacts g_facts[64];
 
@@ -41,6 +41,12 @@ int num_sms() {
   const int n = attribute(dev < 64 ? &g_facts[dev].sms : nullptr, dev,
                           cudaDevAttrMultiProcessorCount);
   return n > 0 ? n : 1;
+}
+
+int64_t l2_bytes() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return attribute(dev < 64 ? &g_facts[dev].l2 : nullptr, dev, cudaDevAttrL2CacheSize);
 }
 
 bool device_ok() {

@@ -9,8 +9,9 @@
 // below change nothing from run to run and every decision is that of exact
 // arithmetic.
 //
-// A row is read from memory once: a cluster of up to sixteen CTAs holds it
-// in shared memory, a slice of whole 1,024-column chunks each, and passes over it
+// A row is read from memory once: a cluster of up to sixteen CTAs takes it, a
+// slice of whole 1,024-column chunks each, keeps it in shared memory (or leaves
+// it to L2, see launch()) and passes over it
 //   1  while it arrives: its maximum and minimum;
 //   2  (top-k, top-p) counts in 2,048 bins equal in y = (max - z) log2(e) / tau;
 //      from the counts and the bins' edges follow the bin of the k-th logit
@@ -46,7 +47,7 @@ constexpr int kUsualParts = 8;    // the most that every GPU lets a cluster have
 constexpr int kBins = 2048;
 constexpr int kList = 2048;       // entries of the list
 constexpr int kBlock = 256;       // columns to a mass
-constexpr size_t kSliceMax = 81920;  // two CTAs an SM
+constexpr size_t kSliceMax = 81920;  // kept in shared memory: two CTAs an SM
 constexpr size_t kSmemLimit = 232448;  // of a CTA alone on its SM
 
 __device__ const FixTable g_fix_table = make_fix_table();
@@ -606,7 +607,7 @@ __host__ __device__ constexpr size_t filter_fixed_bytes(int chunks, int per) {
 }
 
 template <class E, bool kResident>
-__global__ void __launch_bounds__(kFilterThreads, kResident ? 2 : 1)
+__global__ void __launch_bounds__(kFilterThreads, 2)
     filter_sample_kernel(const FilterArgs a) {
   extern __shared__ uint8_t smem[];
   FilterShared& s = *reinterpret_cast<FilterShared*>(smem);
@@ -1193,26 +1194,41 @@ bool wide_clusters() {
 
 template <class E>
 cudaError_t launch(FilterArgs a, int64_t T, cudaStream_t st) {
-  // CTAs to a row: what lets two CTAs share an SM with their slices; more, up
-  // to eight, while the rows do not fill the GPU twice.  Sixteen while half
-  // the SMs hold the rows: 151,936 columns under top-p take 27.8 us in place of
-  // 31.3 (1 row) and 28.3 in place of 32.1 (4), but at 8 rows 35.5 in place of
-  // 32.3 and at 16 rows 55 in place of 40 (a cluster needs its SMs in one GPC).
+  // CTAs to a row, up to eight: as many as are at work at one time, two on an SM
+  // (clusters leave a twentieth of the SMs out).  64 x 151,936 fp32 under top-p
+  // take 77 us with 4, 89 with 2 and, in two waves, 95 with 8; 64 x 8,000 39 us
+  // with 4 and 60 with 8.
   const auto per = [&](int parts) { return (a.chunks + parts - 1) / parts; };
   const auto bytes = [&](int parts) {
     return static_cast<size_t>(per(parts)) * kKeepChunk * sizeof(E);
   };
+  const int64_t ctas = 2 * num_sms();
   int parts = 1;
-  while (parts < kUsualParts && (bytes(parts) > kSliceMax || T * parts < 2 * num_sms()) &&
-         parts < a.chunks)
+  while (parts < kUsualParts && parts < a.chunks && T * 2 * parts <= ctas - ctas / 20) parts *= 2;
+  // One CTA a row leaves that many rows to be read again from L2: two, if two
+  // thirds of it cannot hold them.  1,024 rows with 1 and 2 CTAs: 151,936 fp32
+  // (185 MB at work at a time) 743 and 696 us, bf16 (92 MB) 659 and 665 under
+  // top-p, 635 and 577 with mixed filters; 65,536 fp32 (80 MB) 315 and 365.
+  if (parts == 1 && a.chunks > 1 &&
+      static_cast<double>(T < ctas ? T : ctas) * bytes(1) > l2_bytes() / 3 * 2.0)
+    parts = 2;
+  // (a vocabulary of millions: the chunks' states and masses of two CTAs too)
+  while (parts < kUsualParts && filter_fixed_bytes(a.chunks, per(parts)) > kSmemLimit / 2 - 1024)
     parts *= 2;
+  // Sixteen while half the SMs hold the rows: 151,936 columns under top-p take
+  // 27.8 us in place of 31.3 (1 row) and 28.3 in place of 32.1 (4), but at 8
+  // rows 35.5 in place of 32.3 and at 16 rows 55 in place of 40 (a cluster needs
+  // its SMs in one GPC).
   if (parts == kUsualParts && parts < a.chunks && T * kMaxParts <= num_sms() / 2 &&
-      bytes(parts) + filter_fixed_bytes(a.chunks, per(parts)) <= kSmemLimit && wide_clusters<E>())
+      bytes(parts) <= kSliceMax && wide_clusters<E>())
     parts = kMaxParts;
   a.per = per(parts);
   const size_t fixed = filter_fixed_bytes(a.chunks, a.per);
-  if (fixed + bytes(parts) <= kSmemLimit)
-    return launch_as<E, true>(a, T, parts, fixed + bytes(parts), st);
+  // The slice in shared memory where two CTAs' fit an SM, else read again from
+  // L2: 512 x 151,936 fp32 376 us so, 587 in slices of 76 KB (8 CTAs a row);
+  // 2,048 x 32,003 fp32 431, in slices of 128 KB, one CTA an SM, 488; but bf16
+  // (64 KB) 341 in shared memory and 391 from L2.
+  if (bytes(parts) <= kSliceMax) return launch_as<E, true>(a, T, parts, fixed + bytes(parts), st);
   return launch_as<E, false>(a, T, parts, fixed, st);
 }
 

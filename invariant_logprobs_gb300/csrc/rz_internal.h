@@ -79,6 +79,7 @@ inline size_t decode_bytes(int64_t T, int32_t V) {
 }
 
 int num_sms();
+int64_t l2_bytes();
 bool device_ok();  // current device is sm_103 (or newer family member we compiled for)
 
 bool make_tmap_bf16(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer,

@@ -165,6 +165,26 @@ def test_few_rows_as_in_a_large_batch(rz, V, dtype):
             assert torch.equal(x, y[at])
 
 
+@pytest.mark.parametrize("dtype,V,T", [("f32", 151936, 310), ("bf16", 1 << 21, 310),
+                                       ("f16", 32003, 3000), ("f32", 4097, 150)])
+def test_many_rows_as_alone(rz, dtype, V, T):
+    """Rows of a batch of several waves give what they give alone."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(15)
+    z = (2 * torch.randn(T, V, generator=g, device=DEV, dtype=torch.float32).to(DT[dtype]))
+    f = [FILTERS[r % len(FILTERS)] for r in range(T)]
+    temp = _t([[1.0, 0.7, 0.0][r % 3] for r in range(T)])
+    k, p, mp = (_t([x[i] for x in f], d) for i, d in
+                enumerate([torch.int32, torch.float32, torch.float32]))
+    u = torch.rand(T, generator=g, device=DEV)
+    all_ = _run(rz, z, temp, k, p, mp, u)
+    for lo, n in [(0, 3), (57, 16), (T - 40, 40)]:
+        at = slice(lo, lo + n)
+        few = _run(rz, z[at], temp[at], k[at], p[at], mp[at], u[at])
+        for x, y in zip(few, all_):
+            assert torch.equal(x, y[at])
+
+
 def test_no_filters_at_all_and_row_strides(rz):
     g = torch.Generator(device=DEV)
     g.manual_seed(5)

@@ -1014,52 +1014,97 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs a) {
     }
     g = lo;
   }
-  float M = -INFINITY, L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  // the row's parts: of the prompt, then its own
+  long long x0[2], x1[2], c0[2];
+  int entry[2] = {g, a.P + b}, r[2] = {0, h - hk * a.rep}, count[2];
+#pragma unroll
   for (int part = 0; part < 2; ++part) {
-    const int e = part == 0 ? g : a.P + b;
-    if (e < 0) continue;
-    const int n = (a.clen[e] + kTile - 1) / kTile;
+    const int e = entry[part];
+    const int n = e < 0 ? 0 : (a.clen[e] + kTile - 1) / kTile;
+    count[part] = 0;
     if (n == 0) continue;
     // the row's place in its item, and the item's tiles x0 .. x0 + n - 1
     long long idx = hk;
-    int r = h - hk * a.rep;
     if (part == 0) {
-      const int i = (b - a.cu[g]) * a.rep + r;
+      const int i = (b - a.cu[g]) * a.rep + r[1];
       const int row_tiles = ((a.cu[g + 1] - a.cu[g]) * a.rep + a.row_tile - 1) / a.row_tile;
       idx = static_cast<long long>(hk) * row_tiles + i / a.row_tile;
-      r = i % a.row_tile;
+      r[0] = i % a.row_tile;
     }
-    const long long x0 = a.starts[e] + idx * (n + kItemCost) + kItemCost, x1 = x0 + n;
-    const long long c0 = x0 / per, c1 = (x1 - 1) / per;
-    for (long long c = c0; c <= c1; ++c) {
-      const long long t0 = (c == c0 ? x0 : c * per) - x0;
-      const long long t1 = (c == c1 ? x1 : (c + 1) * per) - x0;
-      for (int gr = 0; gr < kGroups; ++gr) {
-        // (t + head + e) & 1 is the group of tile t
-        if (t1 - t0 < 2 && ((t0 + hk + e) & 1) != gr) continue;
+    x0[part] = a.starts[e] + idx * (n + kItemCost) + kItemCost;
+    x1[part] = x0[part] + n;
+    c0[part] = x0[part] / per;
+    count[part] = static_cast<int>((x1[part] - 1) / per - c0[part] + 1) * kGroups;
+  }
+  // A lane a part for m and l; then, the factors known, all of them read O four
+  // parts at a time (one by one, 4,096 rows of up to 12 parts took 24 us from
+  // cold memory).
+  const int all = count[0] + count[1], col = 4 * lane;
+  float M = -INFINITY, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j0 = 0; j0 < all; j0 += 32) {
+    const int j = j0 + lane;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    const float* src = a.o_base;
+    if (j < all) {
+      const int part = j < count[0] ? 0 : 1;
+      const int q = part == 0 ? j : j - count[0], gr = q % kGroups;
+      const long long first = part == 0 ? c0[0] : c0[1], c = first + q / kGroups;
+      const long long begin = part == 0 ? x0[0] : x0[1], end = part == 0 ? x1[0] : x1[1];
+      const long long t0 = max(c * per, begin) - begin, t1 = min((c + 1) * per, end) - begin;
+      const int e = part == 0 ? entry[0] : entry[1];
+      // (t + head + e) & 1 is the group of tile t
+      if (t1 - t0 >= 2 || ((t0 + hk + e) & 1) == gr) {
+        const bool base = c == first;
         const long long at =
-            c == c0 ? (static_cast<long long>((part == 0 ? 0 : kGroups) + gr) * a.B + b) * a.Hq + h
-                    : (c * kGroups + gr) * kTile + r;
-        const float2 ml = (c == c0 ? a.ml_base : a.ml_extra)[at];
-        const float* src = (c == c0 ? a.o_base : a.o_extra) + at * a.D;
-        const float mn = fmaxf(M, ml.x);
-        if (mn == -INFINITY && !(ml.y != ml.y)) continue;  // no token yet
-        const float ref = mn == -INFINITY ? 0.f : mn;
-        const float f = exp2f(M - ref), fe = exp2f(ml.x - ref);
-        L = L * f + ml.y * fe;
+            base ? (static_cast<long long>((part == 0 ? 0 : kGroups) + gr) * a.B + b) * a.Hq + h
+                 : (c * kGroups + gr) * kTile + (part == 0 ? r[0] : r[1]);
+        ml = (base ? a.ml_base : a.ml_extra)[at];
+        src = (base ? a.o_base : a.o_extra) + at * a.D;
+      }
+    }
+    const bool has = !(ml.x == -INFINITY && ml.y == 0.f);  // a token, or a NaN
+    const float m = fmaxf(M, warp_max(ml.x));
+    const float ref = m == -INFINITY ? 0.f : m;
+    const float f = exp2f(M - ref), fe = has ? exp2f(ml.x - ref) : 0.f;
+    float l = has ? ml.y * fe : 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (lane + 32 * i < a.D) o[i] = o[i] * f + src[lane + 32 * i] * fe;
-        M = mn;
+    for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+    L = L * f + l;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+    M = m;
+    uint32_t who = __ballot_sync(0xffffffffu, has);
+    while (who) {
+      float4 x[4];
+      float w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int from = who ? __ffs(who) - 1 : 0;
+        w[i] = __shfl_sync(0xffffffffu, fe, from);
+        const float* p = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), from));
+        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (who && col < a.D) x[i] = *reinterpret_cast<const float4*>(p + col);
+        who &= who - 1;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o.x += x[i].x * w[i];
+        o.y += x[i].y * w[i];
+        o.z += x[i].z * w[i];
+        o.w += x[i].w * w[i];
       }
     }
   }
-  E* out = static_cast<E*>(a.out) + row * a.D;
   const bool none = M == -INFINITY && L == 0.f;  // no token
   const float inv = none ? 0.f : 1.f / L;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (lane + 32 * i < a.D) put16(out + lane + 32 * i, o[i] * inv);
+  if (col < a.D) {
+    E* out = static_cast<E*>(a.out) + row * a.D + col;
+    put16(out, o.x * inv);
+    put16(out + 1, o.y * inv);
+    put16(out + 2, o.z * inv);
+    put16(out + 3, o.w * inv);
+  }
   if (lane == 0 && a.lse)
     a.lse[row] = none ? -INFINITY : ((M == -INFINITY ? 0.f : M) + log2f(L)) * kLn2;
 }

@@ -55,6 +55,7 @@ RZ_OP_GROUP_DECODE_ATTN = 7
 _lib = None
 _torch_module = None
 _dtype_ids = {}  # torch dtype: RZ_DTYPE_*
+_one_device = None  # whether this machine has one CUDA device
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -214,6 +215,16 @@ def _shape(t, shape, name):
 def _same_device(*ts):
     """All tensors on one CUDA device, and that the current device: the
     library launches on the current device's context."""
+    global _one_device
+    if _one_device is None:
+        _one_device = _torch().cuda.device_count() == 1
+    if _one_device:  # CUDA tensors, as the callers have checked, can only be there
+        tensor = _torch_module.Tensor
+        for t in ts:
+            if type(t) is not tensor and t is not None:
+                break
+        else:
+            return
     dev = None
     for t in ts:
         if t is not None:
@@ -681,14 +692,18 @@ def _dtype_id(t, name, allowed):
     return i
 
 
-def _new(shape, dtype, device, stream):
-    """An output or workspace for work on `stream`: allocated there, so that
-    its memory is neither still in use by nor handed on to another stream."""
-    torch = _torch()
+def _alloc(stream):
+    """torch.empty for outputs and workspace of work on `stream`: allocated
+    there, so that their memory is neither still in use by nor handed on to
+    another stream."""
+    empty = _torch().empty
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return empty
+
+    def on_stream(*args, **kw):
+        with _torch().cuda.stream(stream):
+            return empty(*args, **kw)
+    return on_stream
 
 
 def _rows(t, name):
@@ -735,16 +750,16 @@ def rz_page_tables(lens, new_lens, free_pages, page_size, table, n_slots, slots_
     if err_flag is not None:
         _out(err_flag, int32, "err_flag")
     _same_device(lens, new_lens, free_pages, table, slots_out, cu_out, used_out, err_flag)
-    strm = _stream(stream)
+    strm, new = _stream(stream), _alloc(stream)
     if n_slots < 0:
         raise ValueError("n_slots must not be negative")
     dev = table.device
     if slots_out is None:
-        slots_out = _new(n_slots, torch.int64, dev, stream)
+        slots_out = new(n_slots, dtype=torch.int64, device=dev)
     if cu_out is None:
-        cu_out = _new(B + 1, torch.int64, dev, stream)
+        cu_out = new(B + 1, dtype=torch.int64, device=dev)
     if used_out is None:
-        used_out = _new(1, torch.int32, dev, stream)
+        used_out = new(1, dtype=torch.int32, device=dev)
     st = lib.rz_page_tables(lens.data_ptr(), new_lens.data_ptr(), B, free_pages.data_ptr(),
                             free_pages.numel(), int(page_size), table.data_ptr(), width,
                             slots_out.data_ptr(), n_slots, cu_out.data_ptr(),
@@ -819,17 +834,17 @@ def rz_group_decode_attn(q, k_cache, v_cache, table, lens, prefix_table=None, pr
         _out(err_flag, int32, "err_flag")
     _same_device(q, k_cache, v_cache, table, lens, prefix_table, prefix_lens, cu_group, out,
                  lse_out, ws, err_flag)
-    strm = _stream(stream)
+    strm, new = _stream(stream), _alloc(stream)
     dev = q.device
     if ws is None:
         ws_bytes = _attn_ws(B, D, Hq, P)
-        ws = _new(ws_bytes, torch.uint8, dev, stream)
+        ws = new(ws_bytes, dtype=torch.uint8, device=dev)
     else:
         ws_bytes = _ws_bytes(ws)
     if out is None:
-        out = _new((B, Hq, D), q.dtype, dev, stream)
+        out = new((B, Hq, D), dtype=q.dtype, device=dev)
     if lse_out is None:
-        lse_out = _new((B, Hq), torch.float32, dev, stream)
+        lse_out = new((B, Hq), dtype=torch.float32, device=dev)
     # strides of axes that hold one element mean nothing: give them as 0
     qs = _I64x2(qst[0] if B > 1 else 0, qst[1] if Hq > 1 else 0)
     many = (n_pages > 1, page > 1, Hkv > 1)
@@ -880,16 +895,16 @@ def rz_filter_sample(logits, uniform, temperature=None, top_k=None, top_p=None, 
         _out(err_flag, int32, "err_flag")
     _same_device(logits, uniform, temperature, top_k, top_p, min_p, tokens_out, logprob_out,
                  kept_out, keep_out, err_flag)
-    strm = _stream(stream)
+    strm, new = _stream(stream), _alloc(stream)
     dev = logits.device
     if tokens_out is None:
-        tokens_out = _new(T, torch.int32, dev, stream)
+        tokens_out = new(T, dtype=torch.int32, device=dev)
     if logprob_out is None:
-        logprob_out = _new(T, torch.float32, dev, stream)
+        logprob_out = new(T, dtype=torch.float32, device=dev)
     if kept_out is None:
-        kept_out = _new(T, torch.int32, dev, stream)
+        kept_out = new(T, dtype=torch.int32, device=dev)
     if keep_out is None and want_keep:
-        keep_out = _new((T, words), torch.int32, dev, stream)
+        keep_out = new((T, words), dtype=torch.int32, device=dev)
     st = lib.rz_filter_sample(logits.data_ptr(), ld, dt, T, V, _ptr(temperature), _ptr(top_k),
                               _ptr(top_p), _ptr(min_p), uniform.data_ptr(),
                               tokens_out.data_ptr(), logprob_out.data_ptr(), kept_out.data_ptr(),
@@ -926,11 +941,11 @@ def rz_keep_logprob(logits, tokens, keep=None, temperature=None, logprob_out=Non
     if err_flag is not None:
         _out(err_flag, torch.int32, "err_flag")
     _same_device(logits, tokens, keep, temperature, logprob_out, lse_out, err_flag)
-    strm = _stream(stream)
+    strm, new = _stream(stream), _alloc(stream)
     if logprob_out is None:
-        logprob_out = _new(T, float32, logits.device, stream)
+        logprob_out = new(T, dtype=float32, device=logits.device)
     if lse_out is None:
-        lse_out = _new(T, float32, logits.device, stream)
+        lse_out = new(T, dtype=float32, device=logits.device)
     st = lib.rz_keep_logprob(logits.data_ptr(), ld, dt, T, V, _ptr(keep), _ptr(temperature),
                              tokens.data_ptr(), logprob_out.data_ptr(), lse_out.data_ptr(),
                              _ptr(err_flag), strm)
@@ -958,9 +973,9 @@ def rz_keep_logprob_bwd(logits, tokens, lse, dlogprob, keep=None, temperature=No
     if err_flag is not None:
         _out(err_flag, torch.int32, "err_flag")
     _same_device(logits, tokens, lse, dlogprob, keep, temperature, dlogits_out, err_flag)
-    strm = _stream(stream)
+    strm, new = _stream(stream), _alloc(stream)
     if dlogits_out is None:
-        dlogits_out = _new((T, V), logits.dtype, logits.device, stream)
+        dlogits_out = new((T, V), dtype=logits.dtype, device=logits.device)
     st = lib.rz_keep_logprob_bwd(logits.data_ptr(), ld, dt, T, V, _ptr(keep), _ptr(temperature),
                                  tokens.data_ptr(), lse.data_ptr(), dlogprob.data_ptr(),
                                  dlogits_out.data_ptr(), ldd, _ptr(err_flag), strm)

@@ -25,7 +25,7 @@
 //      the one of them where the running sum passes u.
 //
 // What bounds it is instructions and the steps that one CTA takes for the
-// others, not memory: 512 x 151,936 bf16 under top-p take 343 us where the
+// others, not memory: 512 x 151,936 bf16 under top-p take 338 us where the
 // logits alone are 23 us of bandwidth (some 100 warp instructions for 32
 // logits, nearly half of them a weight of 31 exact bits; issue slots 63% used,
 // the rest barriers and L2).  One row takes 28 us, all of it latency: seven
@@ -977,6 +977,10 @@ __global__ void __launch_bounds__(kFilterThreads, 2)
   // warp a chunk, with its operations in its order)
   const float c = keep_scale(tau);
   const bool vec = kResident || row_aligned(z);
+  // kept is z >= t up to the last of the ties, z >= the next value behind it:
+  // not the sign of z less that (a zero as -0, from which no zero has the sign)
+  const float up = key_value(order_key(cut.t) + 1);
+  const float t_ties = cut.t == 0.f ? -0.f : cut.t, t_up = up == 0.f ? -0.f : up;
   const bool first = u == 0.f;  // the first kept token, whatever its weight rounds to
   have_mass = have_mass && !first;
   uint8_t* keep = a.keep ? reinterpret_cast<uint8_t*>(a.keep + row * a.words) : nullptr;
@@ -993,18 +997,18 @@ __global__ void __launch_bounds__(kFilterThreads, 2)
         float v[8];
         load8(z, vec, n, i, v);  // (-inf past the end)
         uint32_t b = 0;
-        bool tie = false;
+        const int after = cut.last - (v0 + i);  // of the eight, ties up to here
+        const float t = after >= 7 ? t_ties : t_up;
 #pragma unroll
         for (int q = 7; q >= 0; --q) {
-          // the sign of t - z, shifted in
-          b = __funnelshift_l(__float_as_uint(__fsub_rn(cut.t, v[q])), b, 1);
-          tie |= v[q] == cut.t;
+          b = __funnelshift_l(__float_as_uint(__fsub_rn(v[q], t)), b, 1);
           m = fmaxf(m, v[q]);
         }
-        if (tie) {
+        b = ~b & 255u;
+        if (after >= 0 && after < 7) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (v[q] == cut.t && v0 + i + q <= cut.last) b |= 1u << q;
+          for (int q = 0; q < 7; ++q)
+            if (v[q] == cut.t && q <= after) b |= 1u << q;
         }
         bits |= b << (8 * j);
         if (keep) keep[(v0 + i) >> 3] = static_cast<uint8_t>(b);
